@@ -42,6 +42,14 @@ EXPORTS = (
     "star_linear_rope",
     "star_linear_rope_workspace_bytes",
     "star_linear_kv_cache",
+    "star_rope_frequencies",
+    "star_rope_scaled",
+    "star_batch_plan_runs",
+    "star_batch_plan_workspace_bytes",
+    "star_batch_plan",
+    "star_kv8_append",
+    "star_kv8_attend_workspace_bytes",
+    "star_kv8_attend",
     "star_device_status",
     "star_debug_index",
     "star_debug_wait_probe",
@@ -65,6 +73,7 @@ _SZ = ctypes.c_size_t
 _D = ctypes.c_double
 _I64P = ctypes.POINTER(ctypes.c_int64)
 _IP = ctypes.POINTER(ctypes.c_int)
+_DP = ctypes.POINTER(ctypes.c_double)
 
 
 def load(path: str = LIB_PATH):
@@ -129,6 +138,26 @@ def load(path: str = LIB_PATH):
                                            _IP, _I, _I, _I, _I, _D, _P, _SZ, _P]
         lib.star_lse_merge.restype = _I
         lib.star_lse_merge.argtypes = [_P, _P, _I, _P, _P, _I, _I, _I, _I, _P]
+        lib.star_rope_frequencies.restype = _I
+        lib.star_rope_frequencies.argtypes = [_I, _D, _I, _D, _D, _D, _D, _DP, _DP]
+        lib.star_rope_scaled.restype = _I
+        lib.star_rope_scaled.argtypes = [_P, _I64P, _P, _I64P, _P, _I64, _I64, _I, _I, _I, _I, _I,
+                                         _DP, _D, _I, _I, _P]
+        lib.star_batch_plan_runs.restype = _I
+        lib.star_batch_plan_runs.argtypes = [_I, _I, _I]
+        lib.star_batch_plan_workspace_bytes.restype = _SZ
+        lib.star_batch_plan_workspace_bytes.argtypes = [_I]
+        lib.star_batch_plan.restype = _I
+        lib.star_batch_plan.argtypes = [_P, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _I, _P, _I,
+                                        _P, _P, _P, _SZ, _P]
+        lib.star_kv8_append.restype = _I
+        lib.star_kv8_append.argtypes = [_P, _I64P, _P, _I64P, _I, _I, _I, _P, _P, _I, _P, _P, _P,
+                                        _P, _I, _I, _I, _P, _SZ, _P]
+        lib.star_kv8_attend_workspace_bytes.restype = _SZ
+        lib.star_kv8_attend_workspace_bytes.argtypes = [_I, _I, _I, _I, _I, _I]
+        lib.star_kv8_attend.restype = _I
+        lib.star_kv8_attend.argtypes = [_P, _I64P, _I, _P, _P, _I, _P, _I, _P, _P, _P, _P, _I, _I,
+                                        _I, _I, _I, _I, _I, _I, _P, _P, _P, _SZ, _P]
         lib.star_device_status.restype = _I
         lib.star_device_status.argtypes = [_P, _P]
         lib.star_debug_wait_probe.restype = _I

@@ -24,8 +24,10 @@ LIB = os.path.join(HERE, "libstar.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cu", "rope.cu", "lse_merge.cu", "phase2_decode.cu", "phase1_sm100.cu", "noalloc.cu",
-           "stack.cu", "gemm_sm100.cu"]
-HEADERS = ["star_common.cuh", "star_index.cuh", "star_kernels.cuh", "rope_math.cuh", "star_plan.h"]
+           "stack.cu", "gemm_sm100.cu", "kv8_api.cu", "rope_scaled.cu", "batch_plan.cu",
+           "kv8_append.cu", "kv8_decode.cu"]
+HEADERS = ["star_common.cuh", "star_index.cuh", "star_kernels.cuh", "rope_math.cuh", "star_plan.h",
+           "kv8_kernels.cuh", "kv8_codes.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

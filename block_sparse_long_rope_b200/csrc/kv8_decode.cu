@@ -1,0 +1,666 @@
+// Attention of a few new tokens of each request over its 8-bit pages.
+//
+// With codes K, V of page j and scales ks_j, vs_j, row r of a (request, KV head)
+// with query q sees
+//   s = ks_j (q . K) / sqrt(D),  o = sum e^(s - m) vs_j V / sum e^(s - m).
+// Bound: HBM, one byte an element of K and V. The design keeps that stream
+// going:
+//  * The T * g (token, query head) rows of a (request, KV head) form one tile of
+//    8 or 16 rows, so each code is read once for all of them; further rows make
+//    further tiles.
+//  * Work is cut by tiles of 128 keys: CTA c owns an equal contiguous range of
+//    the (request, head, row tile, key tile) list, whatever the lengths. Each
+//    CTA finds its range from the lengths itself. A CTA that holds a whole
+//    unit writes its output; parts of a unit go to the workspace, and the last
+//    CTA to finish one joins its parts in order.
+//  * Each of the 8 warps takes 16 keys of a tile and streams them through its
+//    own ring with cp.async: a thread reads back only what it copied, in the
+//    layout of its matrix fragments, so nothing waits for other warps and
+//    shared memory has no bank conflicts. Pages need only be 16 rows.
+//  * The products are mma.m16n8k16 with keys (then head elements) as the 16
+//    rows and query rows as the 8 columns, S^T = K q^T and O^T = V^T P^T: 8 query
+//    rows waste nothing, and the accumulators are a quarter of a 16-row tile's.
+//    Codes become fp16 without rounding; q, scaled by a power of two to just
+//    below 2^15, keeps all its bits for elements down to 2^-29 of the row's
+//    largest; P^T comes from S^T by an 8x8 transposition in registers.
+//  * P is rounded to fp16 under 2^11, so that a weight keeps full precision
+//    down to 2^-25 of the largest, and is not flushed before 2^-35: a long flat
+//    tail behind one peak still adds up. The running maximum moves only when
+//    it grows by more than 2^4, so P < 2^15 stays finite.
+//  * V scales enter through P as the ratio to a running reference; beyond
+//    [2^-12, 1] the reference moves and O is rescaled.
+#include <math.h>
+
+#include <atomic>
+
+#include "kv8_codes.cuh"
+#include "kv8_kernels.cuh"
+#include "star_kernels.cuh"
+
+namespace star {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr float kPShift = 11.f;  // P is held as 2^11 e^(s - m)
+constexpr float kSlack = 4.f;    // growth of the maximum (log2) before it moves
+
+template <int D>
+struct Cfg {
+  // one warp's stage: 16 keys of K codes, then of V codes, then the two scales
+  static constexpr int kCodes = 16 * D * 2;
+  static constexpr int kStage = kCodes + 16;
+  static constexpr int kRing = kStages * kStage;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// 0xff in each byte of four e4m3 codes that is NaN.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// What a CTA needs of one request.
+struct Request {
+  int q0, T, kv, row_tiles, tiles;  // tiles: key tiles of every row tile, at least 1
+};
+template <int kRows>
+__device__ __forceinline__ Request request_of(const Kv8AttendParams& p, int b, bool* bad) {
+  Request r;
+  const int c0 = p.cu_new[b], c1 = p.cu_new[b + 1];
+  r.q0 = c0;
+  r.T = c1 - c0;
+  r.kv = p.kv_len[b];
+  *bad = c0 < 0 || c1 < c0 || c1 > p.n_tokens || r.T > p.max_new || r.kv < 0 || r.kv > p.max_kv;
+  if (*bad) r.T = 0;
+  r.row_tiles = ceil_div(r.T * p.g, kRows);
+  r.tiles = imax(1, ceil_div(r.kv, kKv8Tile));
+  return r;
+}
+
+}  // namespace
+
+template <int D, int kType, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+    kv8_decode_kernel(const __grid_constant__ Kv8AttendParams p) {
+  using C = Cfg<D>;
+  constexpr int kRows = 8 * NT;
+  constexpr int kSteps = D / 16;  // k-steps of S^T, and 16-row tiles of O^T
+  constexpr int kWords = D / 16;  // 32-bit words of a thread's share of a K row
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* prefix = reinterpret_cast<int*>(smem + kWarps * C::kRing);  // [B + 1] tiles before request b
+  __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+  __shared__ int warp_tiles[kWarps];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gq = lane >> 2, t4 = lane & 3;
+  const int P = 1 << p.page_shift;
+
+  // ---- tiles before each request
+  {
+    const int per = ceil_div(p.B, kThreads);
+    const int b0 = imin(p.B, tid * per), b1 = imin(p.B, b0 + per);
+    int mine = 0;
+    bool any_bad = false;
+    for (int b = b0; b < b1; ++b) {
+      bool bad;
+      const Request r = request_of<kRows>(p, b, &bad);
+      mine += p.Hkv * r.row_tiles * r.tiles;
+      any_bad |= bad;
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(p.status, kDevBounds);
+    if (tid == 0 && blockIdx.x == 0) p.status[1] = p.header_bytes;
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += up;
+    }
+    if (lane == 31) warp_tiles[warp] = inc;
+    __syncthreads();
+    int at = inc - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) at += warp_tiles[w];
+      total += warp_tiles[w];
+    }
+    for (int b = b0; b < b1; ++b) {
+      bool bad;
+      const Request r = request_of<kRows>(p, b, &bad);
+      prefix[b] = at;
+      at += p.Hkv * r.row_tiles * r.tiles;
+    }
+    if (tid == 0) prefix[p.B] = total;
+    __syncthreads();
+  }
+  const int total = prefix[p.B];
+  const int G = imin(static_cast<int>(gridDim.x), total);  // CTAs with work
+  if (static_cast<int>(blockIdx.x) >= G) return;
+  const int begin = static_cast<int>(static_cast<long long>(blockIdx.x) * total / G);
+  const int end = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * total / G);
+
+  // ---- this warp's ring
+  uint8_t* ring = smem + warp * C::kRing;
+  const uint32_t ring_u32 = smem_u32(ring);
+
+  // cursors over the tile list: request, unit (head, row tile) in it, key tile
+  struct Cursor {
+    int b, unit, tile;
+    Request r;
+  };
+  auto locate = [&](int at) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    Cursor c;
+    bool bad;
+    c.b = lo;
+    c.r = request_of<kRows>(p, lo, &bad);
+    c.unit = (at - prefix[lo]) / c.r.tiles;
+    c.tile = (at - prefix[lo]) - c.unit * c.r.tiles;
+    return c;
+  };
+  auto advance = [&](Cursor& c, int next) {  // to list index next < end
+    if (++c.tile < c.r.tiles) return;
+    c.tile = 0;
+    if (++c.unit < p.Hkv * c.r.row_tiles) return;
+    c.unit = 0;
+    bool bad;
+    do ++c.b;
+    while (prefix[c.b + 1] <= next);  // requests without work
+    c.r = request_of<kRows>(p, c.b, &bad);
+  };
+
+  // ---- the copies run kStages - 1 tiles ahead; page numbers one further
+  Cursor pf = locate(begin);
+  int pf_at = begin;
+  auto page_of = [&](const Cursor& c) -> int {
+    const int key0 = c.tile * kKv8Tile + 16 * warp;
+    return key0 < c.r.kv ? p.table[static_cast<size_t>(c.b) * p.max_pages + (key0 >> p.page_shift)] : 0;
+  };
+  int pf_page = page_of(pf);
+  auto issue = [&](int stage) {
+    if (pf_at < end) {
+      const int key0 = pf.tile * kKv8Tile + 16 * warp;
+      const int kvh = pf.unit / pf.r.row_tiles;
+      const uint32_t dst = ring_u32 + stage * C::kStage;
+      if (key0 < pf.r.kv) {
+        const bool ok = pf_page >= 0 && pf_page < p.num_pages;
+        const size_t unit = static_cast<size_t>(ok ? pf_page : 0) * p.Hkv + kvh;
+        const size_t row = (unit << p.page_shift) + (key0 & (P - 1));
+        const uint8_t* kb = p.k_pages + row * D;
+        const uint8_t* vb = p.v_pages + row * D;
+        const int left = pf.r.kv - key0;  // rows behind the last key read as zero codes
+        if (D == 128) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kr = gq + 8 * (i >> 1), vr = 2 * t4 + (i & 1) + 8 * (i >> 1);
+            cp_async16(dst + i * 512 + lane * 16, kb + kr * D + (t4 + 4 * (i & 1)) * 16, kr < left ? 16 : 0);
+            cp_async16(dst + 2048 + i * 512 + lane * 16, vb + vr * D + gq * 16, vr < left ? 16 : 0);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int kr = gq + 8 * i;
+            cp_async16(dst + i * 512 + lane * 16, kb + kr * D + t4 * 16, kr < left ? 16 : 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int vr = 2 * t4 + (i & 1) + 8 * (i >> 1);
+            cp_async8(dst + 1024 + i * 256 + lane * 8, vb + vr * D + gq * 8, vr < left ? 8 : 0);
+          }
+        }
+        float* sc = reinterpret_cast<float*>(ring + stage * C::kStage + C::kCodes);
+        if (ok) {
+          if (lane < 2) cp_async4(smem_u32(sc + lane), (lane ? p.v_scale : p.k_scale) + unit);
+        } else if (lane == 0) {  // no such page: its keys are invisible
+          sc[0] = -1.f;
+          atomicOr(p.status, kDevBounds);
+        }
+      }
+      if (++pf_at < end) {
+        advance(pf, pf_at);
+        pf_page = page_of(pf);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) issue(s);
+
+  Cursor cur = locate(begin);
+  int stage = 0, at = begin;
+  while (at < end) {
+    // ---- one segment: the tiles of one unit that this CTA holds
+    const int kvh = cur.unit / cur.r.row_tiles, rt = cur.unit - kvh * cur.r.row_tiles;
+    const int tile0 = cur.tile, seg = imin(cur.r.tiles - tile0, end - at);
+    const int rows = imin(kRows, cur.r.T * p.g - rt * kRows);  // valid rows of the tile
+    const Cursor here = cur;
+    // rows sit at token t = r / g of the request; row r sees keys below its limit
+    const int past = here.r.kv - here.r.T + 1;
+    const int lim_lo = past + (rt * kRows) / p.g;              // the first row's
+    const int lim_hi = past + (rt * kRows + rows - 1) / p.g;   // the last row's
+
+    // ---- q as B fragments: column n = gq is row rt * kRows + 8 * nt + gq
+    uint32_t qf[NT][kSteps][2];
+    float qscale[NT];  // this lane's row (gq): 2^e log2(e) / sqrt(D)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int n = 8 * nt + gq, r = rt * kRows + n;
+      uint32_t w[kSteps * 2];
+#pragma unroll
+      for (int i = 0; i < kSteps * 2; ++i) w[i] = 0u;
+      if (n < rows) {
+        const __nv_bfloat16* src = p.q + (here.r.q0 + r / p.g) * p.qs[0] +
+                                   (kvh * p.g + r % p.g) * p.qs[1] + 16 * t4;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * c + 8 * v);
+            w[8 * c + 4 * v + 0] = x.x;
+            w[8 * c + 4 * v + 1] = x.y;
+            w[8 * c + 4 * v + 2] = x.z;
+            w[8 * c + 4 * v + 3] = x.w;
+          }
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kSteps * 2; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = static_cast<int>(imax(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent
+      // 2^(14 - (e - 127)), kept a normal number: subnormal rows stay small
+      const int up = imin(254, imax(1, 127 + 14 - (e - 127)));
+      const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
+      qscale[nt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        qf[nt][i][0] = pack_half2(bf16_lo(w[2 * i]) * mul, bf16_hi(w[2 * i]) * mul);
+        qf[nt][i][1] = pack_half2(bf16_lo(w[2 * i + 1]) * mul, bf16_hi(w[2 * i + 1]) * mul);
+      }
+    }
+    float fs[NT][2];  // the factors of this thread's two columns, rows 2 t4 and 2 t4 + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      fs[nt][0] = __shfl_sync(0xffffffffu, qscale[nt], 8 * t4);
+      fs[nt][1] = __shfl_sync(0xffffffffu, qscale[nt], 8 * t4 + 4);
+    }
+
+    float o[NT][kSteps][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    float vref = 0.f, inv_vref = 0.f;  // O is held in units of vref
+
+    for (int i = 0; i < seg; ++i) {
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      const uint8_t* st = ring + stage * C::kStage;
+      const int key0 = (tile0 + i) * kKv8Tile + 16 * warp;
+      const float ks = *reinterpret_cast<const volatile float*>(st + C::kCodes);
+      if (key0 < lim_hi && !(ks < 0.f)) {
+        // ---- S^T = K q^T
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        uint32_t k0[kWords], k1[kWords];
+#pragma unroll
+        for (int c = 0; c < kWords / 4; ++c) {
+          const uint4 a = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
+          const uint4 b = *reinterpret_cast<const uint4*>(st + (kWords / 4 + c) * 512 + lane * 16);
+          k0[4 * c] = a.x, k0[4 * c + 1] = a.y, k0[4 * c + 2] = a.z, k0[4 * c + 3] = a.w;
+          k1[4 * c] = b.x, k1[4 * c + 1] = b.y, k1[4 * c + 2] = b.z, k1[4 * c + 3] = b.w;
+        }
+#pragma unroll
+        for (int w = 0; w < kSteps; ++w) {
+          uint32_t a0, a1, a2, a3;
+          codes_to_half2<kType>(k0[w], a0, a2);
+          codes_to_half2<kType>(k1[w], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][w][0], qf[nt][w][1]);
+        }
+        // ---- scores in log2 units; masked ones are -inf
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[nt][c] *= fs[nt][c & 1] * ks;
+        if (key0 + 16 > lim_lo) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int r = rt * kRows + 8 * nt + 2 * t4 + (c & 1);
+              const int key = key0 + gq + 8 * (c >> 1);
+              if (key >= past + r / p.g) s[nt][c] = -INFINITY;
+            }
+        }
+        // ---- running maximum, moved only when it grows by more than kSlack
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) grow |= s[nt][c] > m[nt][c & 1] + kSlack;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float t = fmaxf(s[nt][c], s[nt][c + 2]);
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+              t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+              const float mn = fmaxf(m[nt][c], t);
+              const float a = mn == -INFINITY ? 1.f : ex2_approx(m[nt][c] - mn);
+              m[nt][c] = mn;
+              l[nt][c] *= a;
+#pragma unroll
+              for (int j = 0; j < kSteps; ++j) {
+                o[nt][j][c] *= a;
+                o[nt][j][c + 2] *= a;
+              }
+            }
+        }
+        // ---- the V scale as a ratio to the reference
+        const float vs = *reinterpret_cast<const volatile float*>(st + C::kCodes + 4);
+        if (vs > vref || (vs < vref * 0.000244140625f && vs > 0.f)) {
+          const float a = vref / vs;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[nt][j][c] *= a;
+          vref = vs;
+          inv_vref = 1.f / vs;
+        }
+        const float vr = vs * inv_vref;
+        // ---- P^T, by columns of keys
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // (two additions: m - kPShift would be rounded where m is large)
+            const float ref = m[nt][c & 1] == -INFINITY ? 0.f : m[nt][c & 1];
+            e[c] = ex2_approx((s[nt][c] - ref) + kPShift);
+            l[nt][c & 1] += e[c];
+          }
+          pb[nt][0] = transpose8x8(pack_half2(e[0] * vr, e[1] * vr));
+          pb[nt][1] = transpose8x8(pack_half2(e[2] * vr, e[3] * vr));
+        }
+        // ---- O^T += V^T P^T: rows 2j and 2j + 1 of this thread's V bytes
+        // (at the causal edge a NaN code must not meet the weight 0 of rows that
+        // do not see it)
+        constexpr int kVWords = D / 32;  // words of a thread's share of a V row
+        uint32_t v[4][kVWords];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(st + 2048 + r * 512 + lane * 16);
+            v[r][0] = x.x, v[r][1] = x.y, v[r][kVWords - 2] = x.z, v[r][kVWords - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + 1024 + r * 256 + lane * 8);
+            v[r][0] = x.x, v[r][1] = x.y;
+          }
+        }
+        if (kType == STAR_KV8_E4M3 && key0 + 16 > lim_lo && here.r.T > 1) {
+          bool nan = false;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int w = 0; w < kVWords; ++w) nan |= nan_bytes(v[r][w]) != 0;
+          if (__any_sync(0xffffffffu, nan)) {
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              bool sees[NT][2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  sees[nt][c] = key0 + k < past + (rt * kRows + 8 * nt + 2 * t4 + c) / p.g;
+#pragma unroll
+              for (int w = 0; w < kVWords; ++w) {
+                const uint32_t mine = (k & 1) ? ((k & 8) ? v[3][w] : v[1][w]) : ((k & 8) ? v[2][w] : v[0][w]);
+                const uint32_t bytes = nan_bytes(__shfl_sync(0xffffffffu, mine, (lane & 28) + ((k & 7) >> 1)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                      if (((bytes >> (8 * i)) & 1u) && sees[nt][c])
+                        o[nt][2 * w + (i >> 1)][c + 2 * (i & 1)] = __uint_as_float(0x7FFFFFFFu);
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int w = 0; w < kVWords; ++w) v[r][w] &= ~nan_bytes(v[r][w]);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) {
+          uint32_t h[4][2];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) codes_to_half2<kType>(v[r][w], h[r][0], h[r][1]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t a0 = __byte_perm(h[0][x], h[1][x], 0x5410), a1 = __byte_perm(h[0][x], h[1][x], 0x7632);
+            const uint32_t a2 = __byte_perm(h[2][x], h[3][x], 0x5410), a3 = __byte_perm(h[2][x], h[3][x], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * w + x], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          }
+        }
+      }
+      // refill the stage read in the previous step (every lane is past it)
+      issue(stage == 0 ? kStages - 1 : stage - 1);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    // the stage of the segment's last tile is refilled after the next tile: until
+    // then it holds this warp's output
+    const int free_stage = stage == 0 ? kStages - 1 : stage - 1;
+    at += seg;
+    cur.tile += seg - 1;
+    if (at < end) advance(cur, at);
+
+    // ---- the segment's end: join the warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
+        l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);
+        if (gq == 0) {
+          wm[warp][8 * nt + 2 * t4 + c] = m[nt][c];
+          wl[warp][8 * nt + 2 * t4 + c] = l[nt][c];
+        }
+      }
+    __syncthreads();
+    const bool whole = seg == here.r.tiles;
+    // parts of a unit: a CTA's first segment goes to slot 0, a later one to 1
+    const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (at - seg == begin ? 0 : 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float M = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) M = fmaxf(M, wm[x][8 * nt + 2 * t4 + c]);
+        w[c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * vref;
+      }
+      float* mine = reinterpret_cast<float*>(ring + free_stage * C::kStage);  // [8][D]
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<float2*>(mine + (2 * t4 + c) * D + gq * (D / 8) + 2 * j) =
+              make_float2(o[nt][j][c] * w[c], o[nt][j][c + 2] * w[c]);
+      __syncthreads();
+      const int n = tid / (D / 4), d = 4 * (tid % (D / 4));
+      if (n < 8) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) M = fmaxf(M, wm[x][8 * nt + n]);
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+          const float4 y = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + x * C::kRing + free_stage * C::kStage) + n * D + d);
+          sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
+          // (a maximum of -inf: nothing seen, a sum of 0, or only NaN)
+          L += M == -INFINITY ? wl[x][8 * nt + n] : wl[x][8 * nt + n] * ex2_approx(wm[x][8 * nt + n] - M);
+        }
+        if (8 * nt + n < rows) {
+          if (whole) {
+            const int r = rt * kRows + 8 * nt + n, head = kvh * p.g + r % p.g;
+            const size_t token = here.r.q0 + r / p.g;
+            const float inv = L != 0.f ? 1.f / L : 0.f;
+            uint2 y;
+            y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
+            y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
+            *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
+            if (d == 0 && p.lse)
+              p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
+                  L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (part * kRows + 8 * nt + n) * D + d) = sum;
+            if (d == 0)
+              *reinterpret_cast<float2*>(p.part_ml + 2 * (part * kRows + 8 * nt + n)) = make_float2(M, L);
+          }
+        }
+      }
+      __syncthreads();
+    }
+
+    // ---- the last CTA of a cut unit joins its parts in order
+    if (!whole) {
+      const int first_tile = at - seg - tile0, last_tile = first_tile + here.r.tiles - 1;
+      // CTA of list index x: the largest c with floor(c * total / G) <= x
+      const int c0 = static_cast<int>(((first_tile + 1ll) * G - 1) / total);
+      const int c1 = static_cast<int>(((last_tile + 1ll) * G - 1) / total);
+      if (tid == 0) {
+        __threadfence();
+        // a unit is cut at the end of its first CTA, and a CTA's end cuts one unit
+        s_last = atomicInc(p.counters + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last) {
+        // the unit's first part is its CTA's first segment only if the CTA begins there
+        const int begin0 = static_cast<int>(static_cast<long long>(c0) * total / G);
+        const size_t slot0 = 2 * static_cast<size_t>(c0) + (begin0 == first_tile ? 0 : 1);
+        for (int e = tid; e < rows * (D / 4); e += kThreads) {
+          const int n = e / (D / 4), d = 4 * (e % (D / 4));
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          float M = -INFINITY, L = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const size_t at_part = (c == c0 ? slot0 : 2 * static_cast<size_t>(c)) * kRows + n;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at_part));
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + at_part * D + d));
+            const float mn = fmaxf(M, ml.x);
+            if (mn == -INFINITY) {  // nothing seen yet (a sum of 0), or only NaN
+              L += ml.y;
+              continue;
+            }
+            const float a = ex2_approx(M - mn), w = ex2_approx(ml.x - mn);
+            sum = make_float4(sum.x * a + y.x * w, sum.y * a + y.y * w, sum.z * a + y.z * w,
+                              sum.w * a + y.w * w);
+            L = L * a + ml.y * w;
+            M = mn;
+          }
+          const int r = rt * kRows + n, head = kvh * p.g + r % p.g;
+          const size_t token = here.r.q0 + r / p.g;
+          const float inv = L != 0.f ? 1.f / L : 0.f;
+          uint2 y;
+          y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
+          y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
+          *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
+          if (d == 0 && p.lse)
+            p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
+                L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  cp_wait<0>();
+}
+
+namespace {
+template <int D, int kType, int NT>
+cudaError_t launch(const Kv8AttendParams& p, int sms, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(kWarps) * Cfg<D>::kRing + (p.B + 1) * sizeof(int);
+  static std::atomic<bool> raised[64];  // this variant's shared-memory limit, by device
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(
+        kv8_decode_kernel<D, kType, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        static_cast<int>(kWarps * Cfg<D>::kRing + (kMaxRequests + 1) * sizeof(int)));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) raised[dev].store(true, std::memory_order_release);
+  }
+  const int grid = imin(kKv8MaxCtas, (NT == 1 ? 2 : 1) * sms);
+  kv8_decode_kernel<D, kType, NT><<<grid, kThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_kv8_decode(const Kv8AttendParams& p, int D, int kv_type, int rows, int sms,
+                              cudaStream_t stream) {
+  const bool e4m3 = kv_type == STAR_KV8_E4M3, one = rows == 8;
+  if (D == 128) {
+    if (e4m3) return one ? launch<128, STAR_KV8_E4M3, 1>(p, sms, stream) : launch<128, STAR_KV8_E4M3, 2>(p, sms, stream);
+    return one ? launch<128, STAR_KV8_INT8, 1>(p, sms, stream) : launch<128, STAR_KV8_INT8, 2>(p, sms, stream);
+  }
+  if (e4m3) return one ? launch<64, STAR_KV8_E4M3, 1>(p, sms, stream) : launch<64, STAR_KV8_E4M3, 2>(p, sms, stream);
+  return one ? launch<64, STAR_KV8_INT8, 1>(p, sms, stream) : launch<64, STAR_KV8_INT8, 2>(p, sms, stream);
+}
+
+}  // namespace star

@@ -1,0 +1,75 @@
+// Parameter blocks and launchers of the operators that serve a ragged batch
+// from an 8-bit paged cache (internal to the library; the public surface is
+// include/star.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace star {
+
+constexpr int kMaxRequests = 4096;  // requests of one call: their offsets live in shared memory
+
+// ---- rotary with given frequencies --------------------------------------------
+struct RopeScaledParams {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* y;
+  long long xs[3], ys[3];  // element strides of (B, S, H)
+  const int32_t* pos;      // nullable
+  long long pos_stride_b, pos0;
+  int B, S, H, D, rot;
+  int tpc, hpc;            // tokens and heads of one CTA
+  int copy_rest;           // 1: elements from rot on are copied (not in place)
+  float mscale_abs;
+  double mscale, sign;     // sign -1: transposed rotation
+  double inv_freq[64];
+};
+cudaError_t launch_rope_scaled(const RopeScaledParams& p, bool interleaved, cudaStream_t stream);
+
+// ---- batch plan -----------------------------------------------------------------
+struct BatchPlanParams {
+  const int32_t *ctx_len, *new_len, *free_pages, *free_begin;
+  int32_t *table, *cu_new, *pos, *slot, *run_start, *kv_len, *free_next;
+  int B, num_free, page_shift, max_pages, n_cap, run_cap;
+  int* status;        // status word
+  unsigned* ticket;   // finished CTAs; zero between calls
+};
+cudaError_t launch_batch_plan(const BatchPlanParams& p, cudaStream_t stream);
+
+// ---- append -----------------------------------------------------------------------
+struct Kv8AppendParams {
+  const __nv_bfloat16 *k, *v;
+  long long ks[2], vs[2];  // element strides of (token, head)
+  const int32_t *slot, *run_start;
+  uint8_t *k_pages, *v_pages;
+  float *k_scale, *v_scale;
+  int n_tokens, Hkv, run_cap, num_pages, page_shift;
+  int* status;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, int D, int kv_type, cudaStream_t stream);
+
+// ---- attention ----------------------------------------------------------------------
+struct Kv8AttendParams {
+  const __nv_bfloat16* q;
+  long long qs[2];  // element strides of (token, head)
+  const int32_t *cu_new, *kv_len, *table;
+  const uint8_t *k_pages, *v_pages;
+  const float *k_scale, *v_scale;
+  __nv_bfloat16* o;
+  float* lse;
+  int n_tokens, B, Hq, Hkv, g, max_pages, num_pages, page_shift, max_new, max_kv;
+  float scale_log2;     // log2(e) / sqrt(D)
+  int* status;          // status word; status[1] receives header_bytes
+  int header_bytes;     // workspace bytes holding the status block and the counters
+  unsigned* counters;   // [kKv8MaxCtas] finished parts of the unit that is cut at a CTA's end
+  float* part_ml;       // [CTAs][2][rows][2] maximum (log2 units) and sum of a part
+  float* part_o;        // [CTAs][2][rows][D]
+};
+constexpr int kKv8Tile = 128;     // keys of one tile of a CTA: 16 for each of its 8 warps
+constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many
+inline int kv8_decode_rows(int max_new, int g) { return (long long)max_new * g <= 8 ? 8 : 16; }
+cudaError_t launch_kv8_decode(const Kv8AttendParams& p, int D, int kv_type, int rows, int sms,
+                              cudaStream_t stream);
+
+}  // namespace star

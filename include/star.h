@@ -421,6 +421,181 @@ star_status star_linear_rope(const void* x, const void* w, void* y, int M, int N
                              void* cuda_stream);
 
 /*
+ * Serving many requests from an 8-bit paged cache.
+ *
+ * The calls above keep one bf16 cache of equal-length sequences. The five
+ * below serve a ragged batch of requests whose keys and values are held in 8
+ * bits, in pages: star_batch_plan gives each request's new tokens positions
+ * and page rows, star_rope_scaled rotates their queries and keys,
+ * star_kv8_append writes their keys and values into the pages, and
+ * star_kv8_attend attends over the pages. A decode step reads half the bytes
+ * of the bf16 cache.
+ *
+ *   pages   k_pages, v_pages [num_pages, Hkv, page_len, D], 8-bit codes;
+ *           page_len 16, 32, 64 or 128 tokens; D 64 or 128
+ *   scales  k_scale, v_scale fp32 [num_pages, Hkv]: a code stands for
+ *           code * scale. star_kv8_append writes powers of two; star_kv8_attend
+ *           takes any positive normal scale (0: a page of zeros)
+ *   type    kv_type STAR_KV8_E4M3 (finite 8-bit floats up to 448, bit 7 the
+ *           sign, 0x7f and 0xff NaN) or STAR_KV8_INT8 (two's complement,
+ *           -127..127)
+ *   table   block_table int32 [B, max_pages]: request b's token p is row
+ *           p % page_len of page block_table[b, p / page_len]
+ *   tokens  the new tokens of all requests are packed: request b's are rows
+ *           cu_new[b] .. cu_new[b + 1] - 1; rows from cu_new[B] on are padding
+ * At most 4096 requests a call; num_pages * page_len and max_pages * page_len
+ * fit int32. Device arrays of lengths and indices are checked by the kernels:
+ * what they would place outside a buffer is left out and recorded as
+ * STAR_ERR_DEVICE_BOUNDS in the workspace's status word. A workspace is
+ * zero-filled once and serves one call at a time: calls that may run at the
+ * same time (two streams, two graphs) need one each.
+ */
+enum { STAR_KV8_E4M3 = 0, STAR_KV8_INT8 = 1 };
+enum {
+  STAR_ROPE_NONE = 0,   /* f_i = theta^(-2i/rot_dim) */
+  STAR_ROPE_LINEAR = 1, /* f_i / factor */
+  STAR_ROPE_NTK = 2,    /* base theta * factor^(rot_dim/(rot_dim-2)) */
+  STAR_ROPE_YARN = 3,   /* by the turns of a pair within orig_len: see below */
+  STAR_ROPE_LLAMA3 = 4
+};
+
+/*
+ * star_rope_frequencies — inverse frequencies of rot_dim / 2 pairs (host
+ * arithmetic in fp64; nothing is launched), scaled for contexts beyond the
+ * trained length orig_len by `factor`:
+ *   YARN    with d(n) = rot_dim * ln(orig_len / (2 pi n)) / (2 ln theta), lo =
+ *           max(floor(d(a)), 0), hi = min(ceil(d(b)), rot_dim - 1) and r_i =
+ *           clamp((i - lo) / (hi - lo), 0, 1) (hi - lo = 0.001 where they are
+ *           equal): f_i / factor * r_i + f_i * (1 - r_i); a, b are the fast
+ *           and slow turn counts; *mscale = 0.1 ln(factor) + 1
+ *   LLAMA3  with n_i = orig_len * f_i / (2 pi), u_i = clamp((n_i - a) /
+ *           (b - a), 0, 1): (1 - u_i) f_i / factor + u_i f_i; a, b are the low
+ *           and high turn counts
+ * *mscale is 1 except for YARN. inv_freq: host double [rot_dim / 2]. a, b and
+ * orig_len are ignored where the scaling has none. STAR_ERR_INVALID_ARG for an
+ * odd or non-positive rot_dim, rot_dim > 128, values that are not finite and
+ * positive, factor < 1, theta <= 1, NTK with rot_dim 2, YARN with a < b, LLAMA3
+ * with a >= b.
+ */
+star_status star_rope_frequencies(int rot_dim, double theta, int scaling, double factor,
+                                  double orig_len, double a, double b, double* inv_freq,
+                                  double* mscale);
+
+/*
+ * star_rope_scaled — rotary positions with given frequencies, over all or the
+ * leading rot_dim elements of each head, at positions p_s (pos[b *
+ * pos_stride_b + s], or pos0 + s when pos is NULL):
+ *   half         pairs (x_i, x_{i + rot_dim/2}), i < rot_dim / 2
+ *   interleaved  pairs (x_{2i}, x_{2i + 1})
+ *   y_first  = mscale * (x_first cos(p f_i) - x_second sin(p f_i))
+ *   y_second = mscale * (x_second cos(p f_i) + x_first sin(p f_i))
+ * transpose = 1 turns by -p f_i instead, which is the gradient of x given
+ * that of y. Elements from rot_dim on are copied. Angles are fp64 and y the
+ * correctly rounded bf16, as star_rope: with rot_dim = D, mscale 1, the half
+ * layout and unscaled frequencies the bits are star_rope's.
+ * x, y: bf16 [B, S, H, D] with strides as star_rope; in place when x == y and
+ * the strides agree, not overlapping otherwise. rot_dim: a multiple of 16, at
+ * most D. inv_freq: host double [rot_dim / 2], read during the call.
+ * mscale and frequencies finite.
+ */
+star_status star_rope_scaled(const void* x, const int64_t x_stride[3], void* y,
+                             const int64_t y_stride[3], const int32_t* pos, int64_t pos_stride_b,
+                             int64_t pos0, int B, int S, int H, int D, int rot_dim,
+                             const double* inv_freq, double mscale, int interleaved,
+                             int transpose, void* cuda_stream);
+
+/* Entries that run_start of star_batch_plan needs, less one: the write runs
+ * that n_tokens new tokens of B requests can make. */
+int star_batch_plan_runs(int n_tokens, int B, int page_len);
+/* Workspace bytes of star_batch_plan. */
+size_t star_batch_plan_workspace_bytes(int B);
+
+/*
+ * star_batch_plan — one serving step's bookkeeping on the GPU, from request
+ * lengths. Request b has ctx_len[b] cached tokens, in the pages that its row of
+ * block_table lists, and brings new_len[b] >= 0 tokens. Pages that these need
+ * beyond the listed ones are taken, request by request, from free_pages at
+ * index *free_begin on and entered into block_table (in place).
+ *   cu_new[B + 1]   token offsets; kv_len[B] = ctx_len + new_len
+ *   pos[n_cap]      position of each new token (0 beyond the last)
+ *   slot[n_cap]     page * page_len + row of each new token (-1 beyond)
+ *   run_start[run_cap + 1]  first tokens of the write runs: the longest spans of
+ *                   one request's new tokens within one page, in token order;
+ *                   the entries after them hold the token count
+ *   *free_next      *free_begin + the pages taken
+ * All arrays are device int32, n_cap and run_cap host sizes (run_cap >=
+ * star_batch_plan_runs(n_cap, B, page_len)). kv_len may be ctx_len, and
+ * free_next may be free_begin: a captured step then advances with each replay.
+ * No other outputs may overlap inputs or each other.
+ * A step that does not fit (more tokens than n_cap, pages than free_pages
+ * holds, a request beyond max_pages, a negative length) is refused as a
+ * whole: cu_new and run_start are 0, slot -1, kv_len = ctx_len, *free_next =
+ * *free_begin, block_table is untouched and the status word records
+ * STAR_ERR_DEVICE_BOUNDS.
+ */
+star_status star_batch_plan(const int32_t* ctx_len, const int32_t* new_len, int B,
+                            const int32_t* free_pages, int num_free, const int32_t* free_begin,
+                            int page_len, int32_t* block_table, int max_pages, int32_t* cu_new,
+                            int32_t* pos, int32_t* slot, int n_cap, int32_t* run_start,
+                            int run_cap, int32_t* kv_len, int32_t* free_next, void* workspace,
+                            size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * star_kv8_append — writes new tokens' keys (already rotated) and values into
+ * their pages in 8 bits. k, v: bf16 [n_tokens, Hkv, D], element strides
+ * k_stride / v_stride of (token, head), multiples of 8, D contiguous. Run u
+ * (run_start[u] < run_start[u + 1]) writes its tokens to consecutive rows from
+ * slot[run_start[u]] on; a run whose slot is negative is skipped. Per head of
+ * the run's page, with amax over the run's finite values:
+ *   s = 2^ceil(log2(amax / 448)) (127 for int8), at least 2^-100
+ *   a run that begins at row 0 starts the page: its scale becomes s. Otherwise
+ *   the scale becomes max(old, s), and where it grew the earlier rows' codes are
+ *   rounded again: code * old / s.
+ * Codes are the nearest values, ties to even; infinities saturate; a NaN is
+ * stored as NaN (e4m3) or 0 (int8). A page may be written by one run of a call
+ * only. Rows behind the run keep their bytes. workspace: >= 256 bytes (the
+ * status word). Runs outside their page, the tokens or the pages are left out
+ * and recorded as STAR_ERR_DEVICE_BOUNDS.
+ */
+star_status star_kv8_append(const void* k, const int64_t k_stride[2], const void* v,
+                            const int64_t v_stride[2], int n_tokens, int Hkv, int D,
+                            const int32_t* slot, const int32_t* run_start, int run_cap,
+                            void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                            int num_pages, int page_len, int kv_type, void* workspace,
+                            size_t workspace_bytes, void* cuda_stream);
+
+/* Workspace bytes of star_kv8_attend for up to n_tokens new tokens, at most
+ * max_new of one request. */
+size_t star_kv8_attend_workspace_bytes(int B, int n_tokens, int Hq, int Hkv, int D, int max_new);
+
+/*
+ * star_kv8_attend — attention of the new tokens over their requests' pages.
+ * q: bf16 [n_tokens, Hq, D], already rotated, element strides q_stride of
+ * (token, head), multiples of 8. Request b has kv_len[b] tokens in its pages,
+ * its T = cu_new[b + 1] - cu_new[b] new ones the last of them: new token t sees
+ * keys [0, kv_len[b] - T + t + 1) of its request; a row that sees none gets o =
+ * 0, lse = -inf. Scale 1/sqrt(D); query head h uses KV head h / (Hq / Hkv).
+ *   o [n_tokens, Hq, D] bf16, lse [Hq, n_tokens] fp32 (NULL to skip)
+ * Rows from cu_new[B] on are left as they are, and so is what lies in pages
+ * behind kv_len, which may hold anything. max_new bounds T, and max_kv
+ * kv_len (1 .. max_pages * page_len): they choose kernels and grids, lengths
+ * beyond them are an error. Each score is exact up to fp32 accumulation (q and
+ * the codes enter the tensor cores unrounded); weights are rounded to 16 bits
+ * before the product with V; sums and statistics are fp32. Results do not
+ * depend on the order in which blocks run.
+ * A request whose lengths or rows of q do not fit is left out, a page index
+ * outside the pages makes its keys invisible; both record
+ * STAR_ERR_DEVICE_BOUNDS.
+ */
+star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_tokens,
+                            const int32_t* cu_new, const int32_t* kv_len, int B,
+                            const int32_t* block_table, int max_pages, const void* k_pages,
+                            const void* v_pages, const float* k_scale, const float* v_scale,
+                            int num_pages, int page_len, int kv_type, int Hq, int Hkv, int D,
+                            int max_new, int max_kv, void* o, float* lse, void* workspace,
+                            size_t workspace_bytes, void* cuda_stream);
+
+/*
  * star_device_status — synchronises `cuda_stream`, then reads the status
  * bits at the start of `workspace` (a workspace passed to any call; the bits
  * are sticky since the last read) and clears them. After a device error it
