@@ -25,7 +25,7 @@ OBJ_DIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.cu", "rope.cu", "lse_merge.cu", "phase2_decode.cu", "phase1_sm100.cu", "noalloc.cu",
            "stack.cu", "gemm_sm100.cu", "kv8_api.cu", "rope_scaled.cu", "batch_plan.cu",
-           "kv8_append.cu", "kv8_decode.cu"]
+           "kv8_append.cu", "kv8_decode.cu", "kv8_chunk.cu"]
 HEADERS = ["star_common.cuh", "star_index.cuh", "star_kernels.cuh", "rope_math.cuh", "star_plan.h",
            "kv8_kernels.cuh", "kv8_codes.cuh"]
 

@@ -101,8 +101,9 @@ struct AttendLayout {
 constexpr size_t kAttendHeader = star::kStatusBytes + star::kKv8MaxCtas * sizeof(unsigned);
 AttendLayout attend_layout(int Hq, int Hkv, int D, int max_new) {
   AttendLayout l;
-  l.rows = star::kv8_decode_rows(max_new, Hq / Hkv);
-  const size_t parts = 2 * (size_t)star::kKv8MaxCtas * l.rows;
+  l.rows = star::kv8_rows(max_new, Hq / Hkv);
+  const size_t ctas = l.rows == star::kKv8ChunkRows ? star::kKv8ChunkMaxCtas : star::kKv8MaxCtas;
+  const size_t parts = 2 * ctas * l.rows;
   l.part_ml = kAttendHeader;
   l.part_o = l.part_ml + align256(parts * 2 * sizeof(float));
   l.total = l.part_o + align256(parts * D * sizeof(float));
@@ -391,7 +392,9 @@ star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_toke
   p.counters = reinterpret_cast<unsigned*>(ws + star::kStatusBytes);
   p.part_ml = reinterpret_cast<float*>(ws + lay.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + lay.part_o);
-  return launched(star::launch_kv8_decode(p, D, kv_type, lay.rows, sms, static_cast<cudaStream_t>(cuda_stream)),
+  cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  return launched(lay.rows == star::kKv8ChunkRows ? star::launch_kv8_chunk(p, D, kv_type, sms, st)
+                                                  : star::launch_kv8_decode(p, D, kv_type, lay.rows, sms, st),
                   "8-bit attention launch");
 }
 

@@ -66,10 +66,16 @@ struct Kv8AttendParams {
   float* part_ml;       // [CTAs][2][rows][2] maximum (log2 units) and sum of a part
   float* part_o;        // [CTAs][2][rows][D]
 };
-constexpr int kKv8Tile = 128;     // keys of one tile of a CTA: 16 for each of its 8 warps
-constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many
-inline int kv8_decode_rows(int max_new, int g) { return (long long)max_new * g <= 8 ? 8 : 16; }
+constexpr int kKv8Tile = 128;     // keys of one tile of a CTA
+constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many (decode)
+constexpr int kKv8ChunkRows = 256, kKv8ChunkMaxCtas = 160;
+// Rows of a (request, KV head) tile: up to 16 the decode kernel's, else the chunk kernel's.
+inline int kv8_rows(int max_new, int g) {
+  const long long rows = (long long)max_new * g;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : kKv8ChunkRows;
+}
 cudaError_t launch_kv8_decode(const Kv8AttendParams& p, int D, int kv_type, int rows, int sms,
                               cudaStream_t stream);
+cudaError_t launch_kv8_chunk(const Kv8AttendParams& p, int D, int kv_type, int sms, cudaStream_t stream);
 
 }  // namespace star

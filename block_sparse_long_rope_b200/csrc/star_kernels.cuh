@@ -168,7 +168,7 @@ void set_last_error(const char* msg);
 // the first time it is asked for that (slot, device); later calls return at
 // once. Safe to call from several host threads. slot < kAttrSlots names the
 // kernel (one slot per kernel instantiation).
-constexpr int kAttrSlots = 16;  // attention 0-3, GEMM 4-6, decode 8-9
+constexpr int kAttrSlots = 16;  // attention 0-3, GEMM 4-6, decode 8-9, batch plan 10, 8-bit chunk 11-14
 cudaError_t set_smem_attr_once(const void* fn, int slot, int dev, size_t bytes);
 // Rank-2 TMA map of a row-major bf16 matrix (inner x outer elements, rows
 // row_bytes apart) with a box of box_inner x box_outer and 128-byte swizzle;

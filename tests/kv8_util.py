@@ -76,8 +76,9 @@ def make_pages(n, heads, page_len, dim, kind, seed, spread=0.5):
 
 
 def attend_plain(q, cu, kv, table, kp, vp, ks, vs):
-    """o, lse, the weighted sum of |v| (for error bounds) and the largest sum |q k| / sqrt(D) of each
-    row, in float64 on the tensors' device. Keys of a page that does not exist are invisible."""
+    """o, lse and what error bounds need: the weighted sum of |v|, the largest sum |q k| / sqrt(D) of each
+    row, and the unweighted sum of |code| times the largest V scale nearby (see check_attend); in
+    float64 on the tensors' device. Keys of a page that does not exist are invisible."""
     n, Hq, D = q.shape
     P, Hkv, page_len, _ = kp.shape
     g = Hq // Hkv
@@ -86,6 +87,7 @@ def attend_plain(q, cu, kv, table, kp, vp, ks, vs):
     ab = torch.zeros_like(o)
     lse = torch.full((Hq, n), -math.inf, dtype=torch.float64, device=dev)
     mag = torch.zeros(Hq, n, dtype=torch.float64, device=dev)
+    low = torch.zeros_like(o)
     for b in range(len(kv)):
         T, L = cu[b + 1] - cu[b], kv[b]
         if T <= 0 or L <= 0:
@@ -97,6 +99,12 @@ def attend_plain(q, cu, kv, table, kp, vp, ks, vs):
         v = (vp[ids].double() * vs[ids].double()[..., None, None]).transpose(0, 1).reshape(Hkv, -1, D)[:, :L]
         there = real.repeat_interleave(page_len)[:L]
         k, v = (torch.where(there[None, :, None], x, torch.zeros_like(x)) for x in (k, v))
+        sc = vs[ids].double().T.repeat_interleave(page_len, 1)  # [Hkv, keys]: the reference scale's bound
+        sc = torch.nn.functional.pad(sc, (0, -sc.shape[1] % 128))
+        tile = sc.view(Hkv, -1, 128).amax(2, keepdim=True).expand(-1, -1, 128).reshape(Hkv, -1)[:, :L]
+        tile = torch.minimum(tile * 4096, sc.amax(1, keepdim=True))[..., None]
+        code = vp[ids].double().transpose(0, 1).reshape(Hkv, -1, D)[:, :L].abs().nan_to_num() * tile
+        code = torch.where(there[None, :, None], code, torch.zeros_like(code))
         for h in range(Hq):
             qq = q[cu[b]:cu[b + 1], h].double()
             s = qq @ k[h // g].T / math.sqrt(D)
@@ -108,10 +116,11 @@ def attend_plain(q, cu, kv, table, kp, vp, ks, vs):
             rows = torch.arange(cu[b], cu[b + 1], device=dev)[some]
             o[rows, h] = w @ v[h // g]
             ab[rows, h] = w @ v[h // g].abs()
+            low[rows, h] = seen[some].double() @ code[h // g]
             lse[h, rows] = torch.logsumexp(s[some], 1)
             m = (qq.abs() @ k[h // g].abs().T / math.sqrt(D)).masked_fill(~seen, 0.0)
             mag[h, cu[b]:cu[b + 1]] = m.amax(1)
-    return o, lse, ab, mag
+    return o, lse, ab, mag, low
 
 
 def check_attend(o, lse, want):
@@ -121,10 +130,15 @@ def check_attend(o, lse, want):
       as much of itself;
     - a weight is rounded to fp16 (2^-11) after ex2.approx and fp32 roundings (below 2^-20 at scores
       up to a few hundred), o sums weights times values in fp32, and is rounded to bf16 (2^-8);
+    - P is held as 2^11 times the weight (at least) of the largest, so a rounding is never below half of
+      fp16's smallest step, 2^-25: 2^-36 of the largest weight, and of the sum, for each key that a row
+      sees. The V scale enters P as the ratio to a reference scale that is some page's of the request and
+      at most 2^12 times the largest of the tile of 128 keys (`low`: the sum over keys of |code| times
+      that);
     - lse adds a logarithm's fp32 roundings: 2^-21 of its size."""
-    wo, wl, ab, mag = want
+    wo, wl, ab, mag, low = want
     ds = 16 * 2.0 ** -23 * mag.T.unsqueeze(-1)
-    bound = 2.0 ** -8 * wo.abs() + ab * (2.0 ** -11 + 2.0 ** -18 + 2 * ds) + 1e-30
+    bound = 2.0 ** -8 * wo.abs() + ab * (2.0 ** -11 + 2.0 ** -18 + 2 * ds) + 2.0 ** -36 * low + 1e-30
     err = (o.double() - wo).abs()
     assert not torch.isnan(o).any()
     worst = float((err / bound).max())

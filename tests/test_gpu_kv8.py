@@ -377,6 +377,9 @@ def _attend(q, cu, lens, table, kp, vp, ks, vs, max_new=None, max_kv=None, ws=No
     ([5], [5], 1, 1, 64, 16, E4M3), ([40], [2], 4, 1, 128, 16, E4M3), ([130], [4], 8, 2, 64, 64, INT8),
     ([1000, 31], [3, 3], 15, 3, 128, 32, E4M3), ([64], [64], 4, 1, 64, 16, E4M3),
     ([300], [129], 8, 2, 128, 64, E4M3), ([900, 77], [100, 40], 16, 2, 64, 128, INT8),
+    ([20000, 5, 1300], [300, 5, 17], 16, 2, 128, 64, E4M3), ([700] * 5, [33] * 5, 8, 1, 64, 16, INT8),
+    ([4097], [257], 8, 1, 128, 16, E4M3), ([130, 131], [130, 1], 1, 1, 128, 32, INT8),
+    ([9000], [20], 7, 1, 64, 32, E4M3), ([600, 0, 2000], [600, 0, 555], 16, 8, 128, 128, INT8),
     # requests without tokens or keys, rows that see nothing
     ([10, 0, 20, 0], [1, 0, 0, 1], 4, 1, 64, 16, E4M3), ([3], [7], 4, 2, 64, 16, E4M3),
     ([0, 0], [2, 1], 8, 1, 128, 32, INT8), ([0], [40], 4, 1, 64, 16, E4M3)])
@@ -438,7 +441,7 @@ def test_attend_nan_reaches_only_the_rows_that_see_it():
     assert torch.isnan(o[1, 2]).all() and torch.isfinite(o[1, 1]).all()
 
 
-@pytest.mark.parametrize("new", [3, 40])
+@pytest.mark.parametrize("new", [3, 40, 100])
 def test_attend_later_nan_does_not_reach_earlier_tokens(new):
     """A new token's own NaN value row is invisible to the tokens before it."""
     L = 50 + new
@@ -481,9 +484,9 @@ def test_attend_strides_padding_and_repeats():
     fused = torch.zeros(n, 12, 128, dtype=torch.bfloat16, device="cuda")
     fused[:, 2:10] = q
     o, lse, ws = _attend(fused[:, 2:10], cu, lens, *rest, fill=5.0)
-    wo, wl, ab, mag = U.attend_plain(q, cu, lens, *rest)
+    wo, wl, ab, mag, low = U.attend_plain(q, cu, lens, *rest)
     m = cu[-1]
-    U.check_attend(o[:m], lse[:, :m], (wo[:m], wl[:, :m], ab[:m], mag[:, :m]))
+    U.check_attend(o[:m], lse[:, :m], (wo[:m], wl[:, :m], ab[:m], mag[:, :m], low[:m]))
     assert bool((o[cu[-1]:] == 5.0).all()) and bool((lse[:, cu[-1]:] == 5.0).all())
     for _ in range(5):
         o2, lse2, _ = _attend(q, cu, lens, *rest, ws=ws, fill=5.0)

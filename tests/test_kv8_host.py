@@ -227,9 +227,11 @@ def test_run_bound(lib):
 
 
 def test_attend_workspace_bytes(lib):
-    for Hq, Hkv, D, new in ((32, 8, 128, 1), (4, 1, 64, 4), (64, 8, 128, 40)):
-        rows = 8 if new * Hq // Hkv <= 8 else 16
-        want = 256 + 512 * 4 + 1024 * rows * 8 + 1024 * rows * D * 4
+    for Hq, Hkv, D, new in ((32, 8, 128, 1), (4, 1, 64, 4), (64, 8, 128, 1), (64, 8, 128, 40)):
+        rows, parts = {8: (8, 1024), 16: (16, 1024)}.get(new * Hq // Hkv, (256, 320))
+        if new * Hq // Hkv < 8:
+            rows, parts = 8, 1024
+        want = 256 + 512 * 4 + parts * rows * 8 + parts * rows * D * 4
         for B in (1, 16):
             assert star.star_kv8_attend_workspace_bytes(B, B * new, Hq, Hkv, D, new) == want
     assert star.star_kv8_attend_workspace_bytes(0, 1, 1, 1, 64, 1) == 256
