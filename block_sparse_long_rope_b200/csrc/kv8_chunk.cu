@@ -123,7 +123,33 @@ __device__ __forceinline__ void next_unit(const Kv8AttendParams& p, const int* p
 struct Scales {
   float k[8], v[8];  // of the 8 groups of 16 keys; k < 0: no such page
   int nan[4];        // by converter warp: a V code at the causal edge is NaN
+  int flags[4];      // [0]: kFirst, kLast (tile of a segment), kTwo (both slots have rows)
 };
+
+enum { kFirst = 1, kLast = 2, kTwo = 4 };
+
+// D[tmem] (+)= A B with A in shared memory or tensor memory: the descriptors'
+// lower words differ from product to product, the upper word is one constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // SBO 1024, version, SWIZZLE_128B
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
 
 // Instruction descriptor of tcgen05.mma kind::f16 with fp16 A and B, fp32 D.
 constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
@@ -136,14 +162,6 @@ __device__ __forceinline__ void fence_async_shared() {
 // A bounded wait with one answer for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
-}
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t r;
@@ -158,6 +176,106 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 // 0xff in each byte of four e4m3 codes that is NaN.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+}
+
+// The softmax's two passes over a row's 128 scores, 32 at a time from tensor
+// memory (the next 32 on their way). Loops of two such steps, not unrolled:
+// the roles of a block share small instruction caches.
+// Score j in log2 units is s_j fs ks; keys from `seen` on and keys of missing
+// pages (ks < 0) are -inf.
+template <bool kMasked>
+__device__ __forceinline__ float max_of_32(uint32_t (&s)[32], const float* ks, float fs, int seen) {
+  float mt = -INFINITY;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (kMasked) {
+#pragma unroll
+      for (int j = 16 * g; j < 16 * g + 16; ++j)
+        if (j >= seen || ks[g] < 0.f) s[j] = 0xFF800000u;
+    }
+    const uint32_t* v = s + 16 * g;
+    float a = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+    float b = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+    for (int j = 6; j < 14; j += 4) {
+      a = fmax3(a, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      b = fmax3(b, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+    }
+    a = fmax3(a, b, fmaxf(__uint_as_float(v[14]), __uint_as_float(v[15])));
+    // (-inf times a scale of 0 is no number, and the maximum ignores it)
+    mt = fmaxf(mt, a * (fs * ks[g]));
+  }
+  return mt;
+}
+template <bool kMasked>
+__device__ __forceinline__ float row_max(uint32_t tS, const Scales& ss, float fs, int seen) {
+  uint32_t a[32], b[32];
+  float mt = -INFINITY;
+  tmem_ld32(tS, a);
+#pragma unroll 1
+  for (int q = 0; q < 4; q += 2) {
+    tmem_wait_ld();
+    reg_fence32(a);
+    tmem_ld32(tS + 32 * q + 32, b);
+    mt = fmaxf(mt, max_of_32<kMasked>(a, ss.k + 2 * q, fs, seen - 32 * q));
+    tmem_wait_ld();
+    reg_fence32(b);
+    if (q == 0) tmem_ld32(tS + 64, a);
+    mt = fmaxf(mt, max_of_32<kMasked>(b, ss.k + 2 * q + 2, fs, seen - 32 * q - 32));
+  }
+  return mt;
+}
+// P = 2^(s - rf) times the ratio of the V scale to its reference, as fp16 pairs
+// over the first half of S (columns are read before they are written);
+// returns the sum of 2^(s - rf).
+template <bool kMasked, bool kEven>
+__device__ __forceinline__ void p_of_32(const uint32_t (&s)[32], const float* ks, const float* vs, float fs,
+                                        int seen, uint64_t nref, float ivref, uint64_t (&ls)[2], uint32_t dst) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float f = fs * ks[g], ratio = kEven ? 1.f : vs[g] * ivref;
+    const uint64_t ff = f2_pack(f, f), rr = f2_pack(ratio, ratio);
+#pragma unroll
+    for (int j = 8 * g; j < 8 * g + 8; ++j) {
+      float x0, x1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), ff, nref), x0, x1);
+      if (kMasked) {
+        if (2 * j >= seen || ks[g] < 0.f) x0 = -INFINITY;
+        if (2 * j + 1 >= seen || ks[g] < 0.f) x1 = -INFINITY;
+      }
+      uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
+      ls[j & 1] = f2_add(ls[j & 1], e);
+      if (!kEven) e = f2_mul(e, rr);
+      f2_unpack(e, x0, x1);
+      pk[j] = half2_of(x0, x1);
+    }
+  }
+  tmem_st16(dst, pk);
+}
+template <bool kMasked, bool kEven>
+__device__ __forceinline__ float write_p(uint32_t tS, const Scales& ss, float fs, int seen, float rf,
+                                         float ivref) {
+  uint32_t a[32], b[32];
+  const uint64_t nref = f2_pack(-rf, -rf);
+  uint64_t ls[2] = {0ull, 0ull};
+  tmem_ld32(tS, a);
+#pragma unroll 1
+  for (int q = 0; q < 4; q += 2) {
+    tmem_wait_ld();
+    reg_fence32(a);
+    tmem_ld32(tS + 32 * q + 32, b);
+    p_of_32<kMasked, kEven>(a, ss.k + 2 * q, ss.v + 2 * q, fs, seen - 32 * q, nref, ivref, ls, tS + 16 * q);
+    tmem_wait_ld();
+    reg_fence32(b);
+    if (q == 0) tmem_ld32(tS + 64, a);
+    p_of_32<kMasked, kEven>(b, ss.k + 2 * q + 2, ss.v + 2 * q + 2, fs, seen - 32 * q - 32, nref, ivref, ls,
+                            tS + 16 * q + 16);
+  }
+  float a0, a1, b0, b1;
+  f2_unpack(ls[0], a0, a1);
+  f2_unpack(ls[1], b0, b1);
+  return (a0 + a1) + (b0 + b1);
 }
 
 // Bit d of the result: a NaN code in column 32 * part + d of the V rows of keys
@@ -271,65 +389,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 
   if (warp >= 12) {
     // ------------------------------------------------------------ MMA issuer
-    regs_down<48>();
     if (warp == 12 && lane == 0) {
       constexpr uint32_t idS = idesc_f16(128, 128, 0);  // S = Q K^T, both K-major
       constexpr uint32_t idO = idesc_f16(128, D, 1);    // O += P V, V is N-major
-      const uint32_t q_base = smem_u32(sm), k_base = q_base + C::kOffK, v_base = q_base + C::kOffV;
-      auto kmajor = [&](uint32_t base, int kk) {
-        return sdesc_sw128(base + (kk >> 2) * C::kHalf + (kk & 3) * 32, 16, 1024);
-      };
+      const uint32_t q_lo = desc_lo(smem_u32(sm), 16), k_lo = desc_lo(smem_u32(sm) + C::kOffK, 16);
+      const uint32_t v_lo = desc_lo(smem_u32(sm) + C::kOffV, C::kHalf);
+      // K-major operands: 16 columns are 32 bytes, 64 columns a half tile
       auto issue_s = [&](int x, int st) {
+        const uint32_t a = q_lo + x * (C::kTile >> 4), b = k_lo + st * (C::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + 128 * x, kmajor(q_base + x * C::kTile, kk), kmajor(k_base + st * C::kTile, kk),
-                 idS, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
+          mma_ss_lo(tmem + 128 * x, a + at, b + at, idS, kk > 0 ? 1u : 0u);
+        }
         mma_commit(&s_full[x]);
       };
-      Walk w = walk_to(p, prefix, begin);
-      int slots = rows_of(p, w.r, w.rt) > 128 ? 2 : 1;
-      bool first = true;       // first tile of a segment: O starts anew
-      uint32_t cnt[2] = {0, 0};  // tiles of a slot so far
-      uint32_t segs[2] = {0, 0};
+      uint32_t cnt[2] = {0, 0};   // tiles of a slot so far
+      uint32_t segs[2] = {0, 0};  // segments of a slot so far
       bool ok = mbar_wait(&k_full[0], 0, &abort_flag, p.status);
-      for (int x = 0; ok && x < slots; ++x) {
-        ok = mbar_wait(&q_full[x], 0, &abort_flag, p.status);
-        if (!ok) break;
+      int now = ring[0].flags[0];
+      for (int x = 0; ok && x < (now & kTwo ? 2 : 1); ++x) {
+        if (!(ok = mbar_wait(&q_full[x], 0, &abort_flag, p.status))) break;
+        ++segs[x];
         tc_fence_after();
         issue_s(x, 0);
-        segs[x] = 1;
       }
       if (ok) mma_commit(&k_empty[0]);
       for (int n = 0; ok && n < N; ++n) {
         const int st = n % S, nst = (n + 1) % S;
-        const bool has_next = n + 1 < N, seg_end = w.tile + 1 == w.tiles || !has_next;
-        const int now = slots;
-        bool next_first = false;
-        if (has_next) {
-          if (seg_end) {
-            next_unit(p, prefix, w, begin + n + 1);
-            slots = rows_of(p, w.r, w.rt) > 128 ? 2 : 1;
-            next_first = true;
-          } else {
-            ++w.tile;
-          }
+        int next = 0;
+        if (n + 1 < N) {
           if (!mbar_wait(&k_full[nst], ((n + 1) / S) & 1, &abort_flag, p.status)) break;
+          next = ring[(n + 1) % kRing].flags[0];
         }
         if (!mbar_wait(&v_full[st], (n / S) & 1, &abort_flag, p.status)) break;
-        for (int x = 0; ok && x < 2; ++x) {
-          if (x < now) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == 0 || (now & kTwo)) {
             if (!(ok = mbar_wait(&p_full[x], cnt[x] & 1, &abort_flag, p.status))) break;
             ++cnt[x];
             tc_fence_after();
+            const uint32_t b = v_lo + st * (C::kTile >> 4);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8,
-                     sdesc_sw128(v_base + st * C::kTile + kk * 2048, C::kHalf, 1024), idO,
-                     (!first || kk > 0) ? 1u : 0u);
-            if (seg_end) mma_commit(&o_full[x]);
+              mma_ts_lo(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * (2048 >> 4), idO,
+                        (!(now & kFirst) || kk > 0) ? 1u : 0u);
+            if (now & kLast) mma_commit(&o_full[x]);
           }
-          if (has_next && x < slots) {
-            if (next_first) {
+          if (n + 1 < N && (x == 0 || (next & kTwo))) {
+            if (next & kFirst) {
               if (!(ok = mbar_wait(&q_full[x], segs[x] & 1, &abort_flag, p.status))) break;
               ++segs[x];
             }
@@ -338,9 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
         }
         if (!ok) break;
-        if (has_next) mma_commit(&k_empty[nst]);
+        if (n + 1 < N) mma_commit(&k_empty[nst]);
         mma_commit(&v_empty[st]);
-        first = seg_end;
+        now = next;
       }
       // every MMA in flight ends before tensor memory is released
       mma_commit(&done);
@@ -351,84 +459,104 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     __syncwarp();
   } else if (warp >= 8) {
     // ------------------------------------------------------------ converters
-    regs_down<112>();
     constexpr int kLoads = D / 16;      // 16-byte loads of a thread for a K or V tile
     constexpr int kPerRow = D / 16;     // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kPerRow;
-    const int cw = warp - 8, ch = lane % kPerRow, r0 = 32 * cw + lane / kPerRow;
+    const int cw = warp - 8, ch = lane % kPerRow, rl = lane / kPerRow, r0 = 32 * cw + rl;
     const int P = 1 << p.page_shift;
     struct Tile {
-      int key0, kv, kvh, edge, page[2];  // pages of this warp's two groups of 16 keys
+      int key0, left, kvh, edge, flags, page[2];  // pages of this warp's two groups of 16 keys
     };
     Walk w = walk_to(p, prefix, begin);
-    auto fetch = [&]() {
+    auto real = [&](int page) { return page >= 0 && page < p.num_pages; };
+    auto fetch = [&](int n) {
       Tile t;
-      t.key0 = w.tile * kKv8Tile;
-      t.kv = w.r.kv;
+      t.flags = (n == 0 || w.tile == 0 ? kFirst : 0) | (n + 1 == N || w.tile + 1 == w.tiles ? kLast : 0) |
+                (rows_of(p, w.r, w.rt) > 128 ? kTwo : 0);
+      t.key0 = w.tile * kKv8Tile + 32 * cw;
+      t.left = w.r.kv - t.key0;  // keys from this warp's first one on
       t.kvh = w.kvh;
-      t.edge = t.key0 + kKv8Tile > keys_of_row(p, w.r, w.rt * kRows);
+      t.edge = w.tile * kKv8Tile + kKv8Tile > keys_of_row(p, w.r, w.rt * kRows);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = t.key0 + 32 * cw + 16 * i;
-        t.page[i] = key < t.kv ? p.table[static_cast<size_t>(w.b) * p.max_pages + (key >> p.page_shift)] : 0;
-      }
+      for (int i = 0; i < 2; ++i)
+        t.page[i] = 16 * i < t.left
+                        ? p.table[static_cast<size_t>(w.b) * p.max_pages + ((t.key0 + 16 * i) >> p.page_shift)]
+                        : 0;
       return t;
     };
     auto step = [&](int n) {  // to tile n of this CTA
       if (w.tile + 1 < w.tiles) ++w.tile;
       else next_unit(p, prefix, w, begin + n);
     };
+    // this lane's first 16 codes of a group of 16 keys
+    auto start = [&](const Tile& t, int i) -> size_t {
+      const size_t row = ((static_cast<size_t>(t.page[i]) * p.Hkv + t.kvh) << p.page_shift) +
+                         ((t.key0 + 16 * i) & (P - 1));
+      return (row + rl) * D + 16 * ch;
+    };
     auto load = [&](uint4 (&x)[kLoads], const Tile& t, const uint8_t* pages) {
+      if (t.left >= 32 && real(t.page[0]) && real(t.page[1])) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4* src = reinterpret_cast<const uint4*>(pages + start(t, i));
+#pragma unroll
+          for (int j = 0; j < kLoads / 2; ++j) x[i * (kLoads / 2) + j] = __ldg(src + j * kRowsPer * (D / 16));
+        }
+        return;
+      }
+      // keys behind the last one, and those of missing pages, are zero codes
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int r = r0 + kRowsPer * j, key = t.key0 + r;
-        const int page = t.page[j >= kLoads / 2];
-        x[j] = make_uint4(0u, 0u, 0u, 0u);  // keys behind the last one are zero codes
-        if (key < t.kv && page >= 0 && page < p.num_pages) {
-          const size_t row = ((static_cast<size_t>(page) * p.Hkv + t.kvh) << p.page_shift) + (key & (P - 1));
-          x[j] = __ldg(reinterpret_cast<const uint4*>(pages + row * D) + ch);
-        }
+        const int i = j / (kLoads / 2), r = rl + kRowsPer * j;
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < t.left && real(t.page[i]))
+          x[j] = __ldg(reinterpret_cast<const uint4*>(pages + start(t, i)) +
+                       (j - i * (kLoads / 2)) * kRowsPer * (D / 16));
       }
     };
     // lanes 0, 1: K scales of the warp's groups; lanes 2, 3: V scales
     auto load_scale = [&](const Tile& t) -> float {
       if (lane >= 4) return 0.f;
       const int page = lane & 1 ? t.page[1] : t.page[0];
-      const bool real = page >= 0 && page < p.num_pages;
-      if (!real) {
+      if (!real(page)) {
         atomicOr(p.status, kDevBounds);
         return lane < 2 ? -1.f : 0.f;
       }
-      if (t.key0 + 32 * cw + 16 * (lane & 1) >= t.kv) return 0.f;
+      if (16 * (lane & 1) >= t.left) return 0.f;
       return __ldg((lane < 2 ? p.k_scale : p.v_scale) + static_cast<size_t>(page) * p.Hkv + t.kvh);
     };
+    // Columns 16 ch .. + 15 of a row are chunks c and c + 1 of a 64-column half.
+    // At D 128 eight lanes share a row and two of them a chunk position: the
+    // second half's lanes write in the other order, so the banks differ. Rows of
+    // a thread are 4 apart (8 at D 64), so the swizzle takes two values (one).
+    const bool turn = ch >= 4;
+    uint32_t at[2][2];
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        at[o][c] = (ch >> 2) * C::kHalf + sw128_offset(r0 + kRowsPer * o, ((2 * ch) & 7) + (c ^ (turn ? 1 : 0))) -
+                   128 * kRowsPer * o;
     auto convert = [&](const uint4 (&x)[kLoads], uint8_t* dst) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const int r = r0 + kRowsPer * j;
         uint4 a, b;
-        codes_to_half2<kType>(x[j].x, a.x, a.y);
-        codes_to_half2<kType>(x[j].y, a.z, a.w);
-        codes_to_half2<kType>(x[j].z, b.x, b.y);
-        codes_to_half2<kType>(x[j].w, b.z, b.w);
-        // columns 16 ch .. + 15: chunks c and c + 1 of a 64-column half. At D 128
-        // eight lanes share a row and two of them a chunk position: the second
-        // half's lanes write in the other order, so the banks differ
-        const int c = (2 * ch) & 7;
-        uint8_t* half = dst + (ch >> 2) * C::kHalf;
-        const bool turn = ch >= 4;
-        *reinterpret_cast<uint4*>(half + sw128_offset(r, c + (turn ? 1 : 0))) = turn ? b : a;
-        *reinterpret_cast<uint4*>(half + sw128_offset(r, c + (turn ? 0 : 1))) = turn ? a : b;
+        codes_to_half2<kType>(turn ? x[j].z : x[j].x, a.x, a.y);
+        codes_to_half2<kType>(turn ? x[j].w : x[j].y, a.z, a.w);
+        codes_to_half2<kType>(turn ? x[j].x : x[j].z, b.x, b.y);
+        codes_to_half2<kType>(turn ? x[j].y : x[j].w, b.z, b.w);
+        *reinterpret_cast<uint4*>(dst + at[j & 1][0] + 128 * kRowsPer * j) = a;
+        *reinterpret_cast<uint4*>(dst + at[j & 1][1] + 128 * kRowsPer * j) = b;
       }
     };
     uint4 kx[kLoads], vx[kLoads];
-    Tile cur = fetch(), nxt = cur;
+    Tile cur = fetch(0), nxt = cur;
     load(kx, cur, p.k_pages);
     load(vx, cur, p.v_pages);
     float sc = load_scale(cur);
     if (N > 1) {
       step(1);
-      nxt = fetch();
+      nxt = fetch(1);
     }
     for (int n = 0; n < N; ++n) {
       const int st = n % S;
@@ -439,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       if (lane < 2) ss.k[2 * cw + lane] = sc;
       else if (lane < 4) ss.v[2 * cw + lane - 2] = sc;
       else if (lane == 4) ss.nan[cw] = 0;
+      else if (cw == 0 && lane == 5) ss.flags[0] = cur.flags;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc_full[n % kRing]);
       convert(kx, sm + C::kOffK + st * C::kTile);
@@ -476,12 +605,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       if (n + 1 < N) load(vx, nxt, p.v_pages);
       if (n + 2 < N) {
         step(n + 2);
-        nxt = fetch();
+        nxt = fetch(n + 2);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
-    regs_up<176>();
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
@@ -536,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // keys that the slot's and the unit's first rows see
       const int lim_lo = keys_of_row(p, here.r, here.rt * kRows + 128 * x);
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
-      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f;
+      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f;
       bool nan = false;
       for (int i = 0; active && i < seg; ++i, ++cnt) {
         const int n = n0 + i;
@@ -545,55 +673,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         // (S of tile n is there, so its scales' phase is the last one completed)
         if (!(ok = warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
         tc_fence_after();
-        uint32_t sr[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, sr[q]);
-        float kmin = ss.k[0], vmax = ss.v[0];
+        const int key0 = (here.tile + i) * kKv8Tile, seen = limit - key0;
+        float kmin = ss.k[0], vmax = ss.v[0], vmin = vmax;
 #pragma unroll
         for (int j = 1; j < 8; ++j) {
           kmin = fminf(kmin, ss.k[j]);
           vmax = fmaxf(vmax, ss.v[j]);
+          vmin = fminf(vmin, ss.v[j]);
         }
-        bool scaled = false;  // the factors are applied already
-        tmem_wait_ld();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) reg_fence32(sr[q]);
-
-        const int key0 = (here.tile + i) * kKv8Tile;
-        if (key0 + kKv8Tile > lim_lo || kmin < 0.f) {
-          // masked keys and keys of missing pages are -inf (after the factor, which
-          // may be 0)
-          const int seen = limit - key0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float ks = ss.k[2 * q + (j >> 4)];
-              const float v = __uint_as_float(sr[q][j]) * (fs * ks);
-              sr[q][j] = 32 * q + j < seen && !(ks < 0.f) ? __float_as_uint(v) : 0xFF800000u;
-            }
-          scaled = true;
-        }
-        auto factor = [&](int g) { return scaled ? 1.f : fs * ss.k[g]; };
+        // masked keys and keys of missing pages are -inf
+        const bool masked = key0 + kKv8Tile > lim_lo || kmin < 0.f;
         if (kType == STAR_KV8_E4M3 && key0 + kKv8Tile > unit_lo) {
           if (!(ok = warp_wait(&nan_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
           const int4 flags = *reinterpret_cast<const int4*>(ss.nan);
           nan |= (flags.x | flags.y | flags.z | flags.w) != 0;
         }
         // ---- row maximum in log2 units
-        float mt = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const uint32_t* s = &sr[g >> 1][16 * (g & 1)];
-          float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
-#pragma unroll
-          for (int j = 2; j < 14; j += 4) {
-            a = fmax3(a, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-            b = fmax3(b, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-          }
-          a = fmax3(a, __uint_as_float(s[14]), __uint_as_float(s[15]));
-          mt = fmaxf(mt, fmaxf(a, b) * factor(g));
-        }
+        const float mt = masked ? row_max<true>(tS, ss, fs, seen) : row_max<false>(tS, ss, fs, seen);
         // ---- move the maximum and the V reference; O and the sum follow
         float alpha = 1.f;
         if (mt > m + kSlack) {
@@ -608,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         if (vmax > vref || (vmax < vref * 0.000244140625f && vmax > 0.f)) {
           alpha *= vref / vmax;
           vref = vmax;
+          ivref = 1.f / vmax;
         }
         if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -622,32 +719,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
           tmem_wait_st();
         }
-        const float ivref = vref > 0.f ? 1.f / vref : 0.f;
-        // ---- P = 2^(s f - rf) times the V ratio, fp16, over the first half of S
-        const uint64_t nref = f2_pack(-rf, -rf);
-        uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int g = 2 * q + (j >> 3);
-            const float f = factor(g), ratio = ss.v[g] * ivref;
-            const uint64_t ff = f2_pack(f, f);
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[q][2 * j]), __uint_as_float(sr[q][2 * j + 1])), ff, nref),
-                      x0, x1);
-            const uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
-            ls[j & 1] = f2_add(ls[j & 1], e);
-            f2_unpack(f2_mul(e, f2_pack(ratio, ratio)), x0, x1);
-            pk[j] = half2_of(x0, x1);
-          }
-          tmem_st16(tS + 16 * q, pk);
-        }
-        float a0, a1, b0, b1;
-        f2_unpack(ls[0], a0, a1);
-        f2_unpack(ls[1], b0, b1);
-        l += (a0 + a1) + (b0 + b1);
+        // ---- P, and the row's sum
+        const bool even = vmin == vref && vmax == vref;  // every V ratio is 1
+        l += masked ? write_p<true, false>(tS, ss, fs, seen, rf, ivref)
+             : even ? write_p<false, true>(tS, ss, fs, seen, rf, ivref)
+                    : write_p<false, false>(tS, ss, fs, seen, rf, ivref);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[x]);
