@@ -172,3 +172,24 @@ def check(status: int):
     if status != 0:
         msg = load().star_last_error().decode(errors="replace")
         raise StarError(status, msg)
+
+
+_native_mod = None
+
+
+def native():
+    """The binding's native half (csrc/binding.cpp), bound to the loaded library."""
+    global _native_mod
+    if _native_mod is None:
+        lib = load()
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_native.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m block_sparse_long_rope_b200.build`")
+        import torch  # noqa: F401  (the extension resolves against its libraries)
+
+        from . import _native
+
+        _native.bind(lib._handle)
+        _native_mod = _native
+    return _native_mod

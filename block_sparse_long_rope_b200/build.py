@@ -29,6 +29,12 @@ SOURCES = ["api.cu", "rope.cu", "lse_merge.cu", "phase2_decode.cu", "phase1_sm10
 HEADERS = ["star_common.cuh", "star_index.cuh", "star_kernels.cuh", "rope_math.cuh", "star_plan.h",
            "kv8_kernels.cuh", "kv8_codes.cuh"]
 
+# the binding's native half, a Python extension against the installed torch
+NATIVE_SRC = os.path.join(CSRC, "binding.cpp")
+NATIVE = os.path.join(HERE, "_native.so")
+CXX = os.environ.get("CXX", "g++")
+CXXFLAGS = ["-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-DNDEBUG"]
+
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -105,7 +111,34 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         os.replace(tmp, LIB)
         with open(lib_stamp, "w") as f:
             f.write(digest)
+    build_native(force)
     return LIB
+
+
+def build_native(force: bool = False) -> str:
+    """Compiles _native.so when its source, the flags or the torch it was built against changed."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    cmd = [CXX] + CXXFLAGS + [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                              "-I" + INCLUDE, "-I" + sysconfig.get_path("include"),
+                              "-I" + os.path.join(root, "include"),
+                              "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                              "-I" + os.path.join(cuda, "include"), NATIVE_SRC]
+    libs = ["-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    want = _sha([NATIVE_SRC, os.path.join(INCLUDE, "star.h")],
+                CXXFLAGS + [torch.__version__, sys.version_info[:3]])
+    stamp = NATIVE + ".sha256"
+    if force or not os.path.exists(NATIVE) or _read(stamp) != want:
+        tmp = NATIVE + f".tmp{os.getpid()}"
+        subprocess.check_call(cmd + ["-o", tmp] + libs)
+        os.replace(tmp, NATIVE)
+        with open(stamp, "w") as f:
+            f.write(want)
+    return NATIVE
 
 
 def loaded_matches_sources() -> bool:

@@ -2,7 +2,8 @@
 
 Only argument marshalling happens here: pointers, sizes and the current CUDA
 stream are passed to libstar.so, which validates and launches. PyTorch serves
-for device memory and streams.
+for device memory and streams. The calls of a serving step marshal theirs in
+csrc/binding.cpp.
 """
 import ctypes
 
@@ -343,50 +344,6 @@ def star_phase1_encode_rotated(q_rot, o, k_cache, v_cache, L, block_len, anchor_
 # ---- serving a ragged batch from an 8-bit paged cache ------------------------
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "llama3": 4}
-KV8_TYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
-
-
-def _same_device(named):
-    """The one CUDA device of all tensors given (None entries skipped)."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    return dev
-
-
-class _on:
-    """Makes the tensors' device current for a call and gives its stream: the one passed, or the
-    device's current stream."""
-
-    def __init__(self, dev, stream):
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-        self.dev, self.stream = dev, stream
-
-    def __enter__(self):
-        self.guard = None
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _ints(t, name, n=None):
-    if t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} must have {n} entries, it has {t.numel()}")
 
 
 def star_rope_frequencies(rot_dim, theta, scaling="none", factor=1.0, orig_len=0.0, low_freq=0.0,
@@ -410,27 +367,11 @@ def star_rope_scaled(x, y, inv_freq, mscale=1.0, interleaved=False, transpose=Fa
     """Rotates the leading 2 * len(inv_freq) elements of each head of x[B, S, H, D] at positions
     pos (int32 [S] or [B, S]) or pos0 + s, and copies the rest; transpose turns the other way (the
     gradient). x, y: bf16 views with D contiguous; y may be x."""
-    _bf16(x, "x")
-    _bf16(y, "y")
-    if x.dim() != 4 or y.shape != x.shape:
-        raise ValueError("x and y must have one shape [B, S, H, D]")
-    if x.stride(3) != 1 or y.stride(3) != 1:
-        raise ValueError("head_dim must be contiguous")
-    B, S, H, D = x.shape
-    pos_stride = 0
-    if pos is not None:
-        if pos.dtype != torch.int32 or pos.shape not in ((S,), (B, S)) or \
-                (S > 1 and pos.stride(-1) != 1):
-            raise ValueError("pos must be int32 [S] or [B, S], contiguous in S")
-        pos_stride = pos.stride(0) if pos.dim() == 2 else 0
     if not isinstance(inv_freq, ctypes.Array):
         inv_freq = (ctypes.c_double * len(inv_freq))(*[float(f) for f in inv_freq])
-    dev = _same_device((("x", x), ("y", y), ("pos", pos)))
-    with _on(dev, stream) as st:
-        _abi.check(_abi.load().star_rope_scaled(
-            _ptr(x), _i64x3(x.stride()[:3]), _ptr(y), _i64x3(y.stride()[:3]), _ptr(pos),
-            pos_stride, int(pos0), B, S, H, D, 2 * len(inv_freq), inv_freq, float(mscale),
-            1 if interleaved else 0, 1 if transpose else 0, st))
+    st = _abi.native().rope_scaled(x, y, inv_freq, mscale, interleaved, transpose, pos, pos0, stream)
+    if st:
+        _abi.check(st)
     return y
 
 
@@ -450,48 +391,10 @@ def star_batch_plan(ctx_len, new_len, free_pages, free_begin, page_len, block_ta
     pos[n], slot[n], run_start[runs + 1], kv_len[B] and free_next[1]. kv_len may be ctx_len,
     free_next may be free_begin. A step that does not fit is refused as a whole (see
     include/star.h); star_device_status(workspace) reports it."""
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, W = block_table.shape
-    _ints(block_table, "block_table")
-    _ints(free_pages, "free_pages")
-    n = pos.numel()
-    for t, name, size in ((ctx_len, "ctx_len", B), (new_len, "new_len", B), (kv_len, "kv_len", B),
-                          (cu_new, "cu_new", B + 1), (pos, "pos", n), (slot, "slot", n),
-                          (free_begin, "free_begin", 1), (free_next, "free_next", 1),
-                          (run_start, "run_start", None)):
-        _ints(t, name, size)
-    dev = _same_device((("block_table", block_table), ("ctx_len", ctx_len), ("new_len", new_len),
-                        ("free_pages", free_pages), ("free_begin", free_begin),
-                        ("cu_new", cu_new), ("pos", pos), ("slot", slot),
-                        ("run_start", run_start), ("kv_len", kv_len), ("free_next", free_next),
-                        ("workspace", workspace)))
-    with _on(dev, stream) as st:
-        _abi.check(_abi.load().star_batch_plan(
-            _ptr(ctx_len), _ptr(new_len), B, _ptr(free_pages), free_pages.numel(),
-            _ptr(free_begin), int(page_len), _ptr(block_table), W, _ptr(cu_new), _ptr(pos),
-            _ptr(slot), n, _ptr(run_start), run_start.numel() - 1, _ptr(kv_len), _ptr(free_next),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), st))
-
-
-def _kv8_cache(k_pages, v_pages, k_scale, v_scale):
-    if k_pages.dtype not in KV8_TYPES or v_pages.dtype != k_pages.dtype:
-        raise TypeError("k_pages and v_pages must both be float8_e4m3fn or int8, got "
-                        f"{k_pages.dtype} and {v_pages.dtype}")
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must have one shape [num_pages, Hkv, page_len, D]")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype != torch.float32 or t.shape != k_pages.shape[:2]:
-            raise ValueError(f"{name} must be float32 [num_pages, Hkv]")
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_scale, "k_scale"),
-                    (v_scale, "v_scale")):
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    return KV8_TYPES[k_pages.dtype]
-
-
-def _i64x2(vals):
-    return (ctypes.c_int64 * 2)(*[int(v) for v in vals])
+    st = _abi.native().batch_plan(ctx_len, new_len, free_pages, free_begin, page_len, block_table,
+                                  cu_new, pos, slot, run_start, kv_len, free_next, workspace, stream)
+    if st:
+        _abi.check(st)
 
 
 def star_kv8_append(k, v, slot, run_start, k_pages, v_pages, k_scale, v_scale, workspace,
@@ -499,26 +402,10 @@ def star_kv8_append(k, v, slot, run_start, k_pages, v_pages, k_scale, v_scale, w
     """Writes the new tokens' keys (rotated) and values k, v [n, Hkv, D] (bf16 views, D contiguous)
     into 8-bit pages [num_pages, Hkv, page_len, D] with scales [num_pages, Hkv], at the rows that
     slot[n] and run_start (see star_batch_plan) give."""
-    kind = _kv8_cache(k_pages, v_pages, k_scale, v_scale)
-    pages, Hkv, page_len, D = k_pages.shape
-    for t, name in ((k, "k"), (v, "v")):
-        _bf16(t, name)
-        if t.dim() != 3 or t.shape[1:] != (Hkv, D) or t.shape[0] != k.shape[0]:
-            raise ValueError(f"{name} must be [n, {Hkv}, {D}]")
-        if t.stride(2) != 1:
-            raise ValueError(f"{name} must be contiguous in head_dim")
-    n = k.shape[0]
-    _ints(slot, "slot", n)
-    _ints(run_start, "run_start")
-    dev = _same_device((("k", k), ("v", v), ("slot", slot), ("run_start", run_start),
-                        ("k_pages", k_pages), ("v_pages", v_pages), ("k_scale", k_scale),
-                        ("v_scale", v_scale), ("workspace", workspace)))
-    with _on(dev, stream) as st:
-        _abi.check(_abi.load().star_kv8_append(
-            _ptr(k), _i64x2(k.stride()[:2]), _ptr(v), _i64x2(v.stride()[:2]), n, Hkv, D,
-            _ptr(slot), _ptr(run_start), run_start.numel() - 1, _ptr(k_pages), _ptr(v_pages),
-            _ptr(k_scale), _ptr(v_scale), pages, page_len, kind, _ptr(workspace),
-            workspace.numel() * workspace.element_size(), st))
+    st = _abi.native().kv8_append(k, v, slot, run_start, k_pages, v_pages, k_scale, v_scale, workspace,
+                                  stream)
+    if st:
+        _abi.check(st)
 
 
 def star_kv8_attend_workspace_bytes(B, n_tokens, Hq, Hkv, D, max_new) -> int:
@@ -531,33 +418,10 @@ def star_kv8_attend(q, cu_new, kv_len, block_table, k_pages, v_pages, k_scale, v
     pages: o[n, Hq, D] bf16 and, when given, lse[Hq, n] fp32. Request b's tokens are rows
     cu_new[b] .. cu_new[b + 1] - 1, the last of its kv_len[b] cached ones; max_new and max_kv bound
     both."""
-    kind = _kv8_cache(k_pages, v_pages, k_scale, v_scale)
-    pages, Hkv, page_len, D = k_pages.shape
-    _bf16(q, "q")
-    _bf16(o, "o")
-    if q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1:
-        raise ValueError(f"q must be [n, Hq, {D}], contiguous in head_dim")
-    if o.shape != q.shape or not o.is_contiguous():
-        raise ValueError("o must be contiguous, of q's shape")
-    n, Hq, _ = q.shape
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (Hq, n) or
-                            not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous float32 [{Hq}, {n}]")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, W = block_table.shape
-    _ints(block_table, "block_table")
-    _ints(cu_new, "cu_new", B + 1)
-    _ints(kv_len, "kv_len", B)
-    dev = _same_device((("q", q), ("o", o), ("lse", lse), ("cu_new", cu_new), ("kv_len", kv_len),
-                        ("block_table", block_table), ("k_pages", k_pages), ("v_pages", v_pages),
-                        ("k_scale", k_scale), ("v_scale", v_scale), ("workspace", workspace)))
-    with _on(dev, stream) as st:
-        _abi.check(_abi.load().star_kv8_attend(
-            _ptr(q), _i64x2(q.stride()[:2]), n, _ptr(cu_new), _ptr(kv_len), B, _ptr(block_table), W,
-            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), pages, page_len, kind, Hq,
-            Hkv, D, int(max_new), int(max_kv), _ptr(o), _ptr(lse), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), st))
+    st = _abi.native().kv8_attend(q, cu_new, kv_len, block_table, k_pages, v_pages, k_scale, v_scale, o,
+                                  workspace, max_new, max_kv, lse, stream)
+    if st:
+        _abi.check(st)
     return o
 
 

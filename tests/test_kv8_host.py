@@ -286,6 +286,10 @@ def test_other_binding_refusals():
     with pytest.raises(ValueError):
         star.star_kv8_append(bf(1, 2, 64), bf(1, 2, 64), a["cu_new"], a["cu_new"], a["k_pages"],
                              a["v_pages"], a["k_scale"], a["v_scale"], a["workspace"])
+    with pytest.raises(TypeError):
+        star.star_rope_scaled(bf(1, 2, 3, 64), bf(1, 2, 3, 64), (ctypes.c_float * 16)())
+    with pytest.raises(TypeError):
+        star.star_rope_scaled(None, bf(1, 2, 3, 64), f)
     i = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
     with pytest.raises(ValueError):
         star.star_batch_plan(i(1), i(2), i(4), i(1), 16, a["block_table"], i(2), i(4), i(4), i(5),
