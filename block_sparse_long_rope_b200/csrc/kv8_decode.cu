@@ -14,9 +14,11 @@
 //    unit writes its output; parts of a unit go to the workspace, and the last
 //    CTA to finish one joins its parts in order.
 //  * Each of the 8 warps takes 16 keys of a tile and streams them through its
-//    own ring with cp.async: a thread reads back only what it copied, in the
-//    layout of its matrix fragments, so nothing waits for other warps and
-//    shared memory has no bank conflicts. Pages need only be 16 rows.
+//    own ring with cp.async, so nothing waits for other warps and pages need
+//    only be 16 rows. An instruction copies 512 contiguous bytes (64-byte pieces
+//    in fragment order reached 4.6 TB/s instead of 7.0) and swizzles their 16-byte
+//    pieces, and the keys are assigned to matrix rows so that the fragments'
+//    reads have no bank conflicts either.
 //  * The products are mma.m16n8k16 with keys (then head elements) as the 16
 //    rows and query rows as the 8 columns, S^T = K q^T and O^T = V^T P^T: 8 query
 //    rows waste nothing, and the accumulators are a quarter of a 16-row tile's.
@@ -58,9 +60,6 @@ struct Cfg {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -86,6 +85,18 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Offset of 16-byte piece c of row r in a stage's 16 rows of D bytes: the pieces
+// of a 128-byte line trade places by the line's number.
+template <int D>
+__device__ __forceinline__ uint32_t piece(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+// Key of matrix row i (0..7): at D 128 neighbours are 4 apart, in other banks.
+template <int D>
+__device__ __forceinline__ int key_of(int i) {
+  return D == 128 ? ((i & 1) << 2) | (i >> 1) : i;
 }
 
 // 0xff in each byte of four e4m3 codes that is NaN.
@@ -228,24 +239,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         const uint8_t* kb = p.k_pages + row * D;
         const uint8_t* vb = p.v_pages + row * D;
         const int left = pf.r.kv - key0;  // rows behind the last key read as zero codes
-        if (D == 128) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kr = gq + 8 * (i >> 1), vr = 2 * t4 + (i & 1) + 8 * (i >> 1);
-            cp_async16(dst + i * 512 + lane * 16, kb + kr * D + (t4 + 4 * (i & 1)) * 16, kr < left ? 16 : 0);
-            cp_async16(dst + 2048 + i * 512 + lane * 16, vb + vr * D + gq * 16, vr < left ? 16 : 0);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int kr = gq + 8 * i;
-            cp_async16(dst + i * 512 + lane * 16, kb + kr * D + t4 * 16, kr < left ? 16 : 0);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int vr = 2 * t4 + (i & 1) + 8 * (i >> 1);
-            cp_async8(dst + 1024 + i * 256 + lane * 8, vb + vr * D + gq * 8, vr < left ? 8 : 0);
-          }
+        for (int i = 0; i < D / 32; ++i) {  // 512 bytes: 4 rows, or 8 of D 64
+          const int r = (512 / D) * i + lane / (D / 16), bytes = r < left ? 16 : 0;
+          const uint32_t to = dst + piece<D>(r, lane % (D / 16));
+          cp_async16(to, kb + 512 * i + 16 * lane, bytes);
+          cp_async16(to + 16 * D, vb + 512 * i + 16 * lane, bytes);
         }
         float* sc = reinterpret_cast<float*>(ring + stage * C::kStage + C::kCodes);
         if (ok) {
@@ -349,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
         uint32_t k0[kWords], k1[kWords];
 #pragma unroll
         for (int c = 0; c < kWords / 4; ++c) {
-          const uint4 a = *reinterpret_cast<const uint4*>(st + c * 512 + lane * 16);
-          const uint4 b = *reinterpret_cast<const uint4*>(st + (kWords / 4 + c) * 512 + lane * 16);
+          const uint4 a = *reinterpret_cast<const uint4*>(st + piece<D>(key_of<D>(gq), t4 + 4 * c));
+          const uint4 b = *reinterpret_cast<const uint4*>(st + piece<D>(key_of<D>(gq) + 8, t4 + 4 * c));
           k0[4 * c] = a.x, k0[4 * c + 1] = a.y, k0[4 * c + 2] = a.z, k0[4 * c + 3] = a.w;
           k1[4 * c] = b.x, k1[4 * c + 1] = b.y, k1[4 * c + 2] = b.z, k1[4 * c + 3] = b.w;
         }
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int r = rt * kRows + 8 * nt + 2 * t4 + (c & 1);
-              const int key = key0 + gq + 8 * (c >> 1);
+              const int key = key0 + key_of<D>(gq) + 8 * (c >> 1);
               if (key >= past + r / p.g) s[nt][c] = -INFINITY;
             }
         }
@@ -432,18 +431,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           pb[nt][0] = transpose8x8(pack_half2(e[0] * vr, e[1] * vr));
           pb[nt][1] = transpose8x8(pack_half2(e[2] * vr, e[3] * vr));
         }
-        // ---- O^T += V^T P^T: rows 2j and 2j + 1 of this thread's V bytes
+        // ---- O^T += V^T P^T: the keys of matrix columns 2 t4, 2 t4 + 1 and 8 more;
+        // lanes with `turn` read each pair in the other order (for the banks)
         // (at the causal edge a NaN code must not meet the weight 0 of rows that
         // do not see it)
         constexpr int kVWords = D / 32;  // words of a thread's share of a V row
+        const int turn = D == 128 ? gq & 1 : (gq >> 1) & 1;
         uint32_t v[4][kVWords];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
+          const int row = key_of<D>(2 * t4 + ((r & 1) ^ turn)) + 8 * (r >> 1);
           if (D == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(st + 2048 + r * 512 + lane * 16);
+            const uint4 x = *reinterpret_cast<const uint4*>(st + 16 * D + piece<D>(row, gq));
             v[r][0] = x.x, v[r][1] = x.y, v[r][kVWords - 2] = x.z, v[r][kVWords - 1] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + 1024 + r * 256 + lane * 8);
+            const uint2 x = *reinterpret_cast<const uint2*>(st + 16 * D + piece<D>(row, gq >> 1) + 8 * (gq & 1));
             v[r][0] = x.x, v[r][1] = x.y;
           }
         }
@@ -461,10 +463,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                  sees[nt][c] = key0 + k < past + (rt * kRows + 8 * nt + 2 * t4 + c) / p.g;
+                  sees[nt][c] = key0 + key_of<D>(k & 7) + (k & 8) < past + (rt * kRows + 8 * nt + 2 * t4 + c) / p.g;
 #pragma unroll
               for (int w = 0; w < kVWords; ++w) {
-                const uint32_t mine = (k & 1) ? ((k & 8) ? v[3][w] : v[1][w]) : ((k & 8) ? v[2][w] : v[0][w]);
+                // k: matrix column, held by lane (k % 8) / 2 of this lane's four
+                const int second = (k & 1) ^ turn;
+                const uint32_t mine = second ? ((k & 8) ? v[3][w] : v[1][w]) : ((k & 8) ? v[2][w] : v[0][w]);
                 const uint32_t bytes = nan_bytes(__shfl_sync(0xffffffffu, mine, (lane & 28) + ((k & 7) >> 1)));
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -482,19 +486,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
               for (int w = 0; w < kVWords; ++w) v[r][w] &= ~nan_bytes(v[r][w]);
           }
         }
+        // two keys' bytes interleaved become a fragment's pairs
+        const uint32_t even = turn ? 0x1504u : 0x5140u, odd = turn ? 0x3726u : 0x7362u;
 #pragma unroll
-        for (int w = 0; w < kVWords; ++w) {
-          uint32_t h[4][2];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) codes_to_half2<kType>(v[r][w], h[r][0], h[r][1]);
+        for (int w = 0; w < kVWords; ++w)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t a0 = __byte_perm(h[0][x], h[1][x], 0x5410), a1 = __byte_perm(h[0][x], h[1][x], 0x7632);
-            const uint32_t a2 = __byte_perm(h[2][x], h[3][x], 0x5410), a3 = __byte_perm(h[2][x], h[3][x], 0x7632);
+            const uint32_t sel = x ? odd : even;
+            uint32_t a0, a1, a2, a3;
+            codes_to_half2<kType>(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
+            codes_to_half2<kType>(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * w + x], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
           }
-        }
       }
       // refill the stage read in the previous step (every lane is past it)
       issue(stage == 0 ? kStages - 1 : stage - 1);
