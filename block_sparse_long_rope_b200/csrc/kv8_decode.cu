@@ -51,10 +51,12 @@ constexpr float kSlack = 4.f;    // growth of the maximum (log2) before it moves
 
 template <int D>
 struct Cfg {
-  // one warp's stage: 16 keys of K codes, then of V codes, then the two scales
-  static constexpr int kCodes = 16 * D * 2;
-  static constexpr int kStage = kCodes + 16;
+  // one warp's stage: 16 keys of K codes, then of V codes, in whole 128-byte lines;
+  // the two scales of every stage come after the rings
+  static constexpr int kStage = 16 * D * 2;
   static constexpr int kRing = kStages * kStage;
+  static constexpr int kScales = kWarps * kRing;
+  static constexpr int kPrefix = kScales + kWarps * kStages * 8;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -131,8 +133,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   constexpr int kRows = 8 * NT;
   constexpr int kSteps = D / 16;  // k-steps of S^T, and 16-row tiles of O^T
   constexpr int kWords = D / 16;  // 32-bit words of a thread's share of a K row
-  extern __shared__ __align__(16) uint8_t smem[];
-  int* prefix = reinterpret_cast<int*>(smem + kWarps * C::kRing);  // [B + 1] tiles before request b
+  extern __shared__ __align__(128) uint8_t smem[];
+  int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);  // [B + 1] tiles before request b
   __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
   __shared__ int warp_tiles[kWarps];
   __shared__ int s_last;
@@ -187,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   // ---- this warp's ring
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_u32 = smem_u32(ring);
+  float* scales = reinterpret_cast<float*>(smem + C::kScales) + warp * kStages * 2;  // K and V scale by stage
 
   // cursors over the tile list: request, unit (head, row tile) in it, key tile
   struct Cursor {
@@ -246,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
           cp_async16(to, kb + 512 * i + 16 * lane, bytes);
           cp_async16(to + 16 * D, vb + 512 * i + 16 * lane, bytes);
         }
-        float* sc = reinterpret_cast<float*>(ring + stage * C::kStage + C::kCodes);
+        float* sc = scales + 2 * stage;
         if (ok) {
           if (lane < 2) cp_async4(smem_u32(sc + lane), (lane ? p.v_scale : p.k_scale) + unit);
         } else if (lane == 0) {  // no such page: its keys are invisible
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       __syncwarp();
       const uint8_t* st = ring + stage * C::kStage;
       const int key0 = (tile0 + i) * kKv8Tile + 16 * warp;
-      const float ks = *reinterpret_cast<const volatile float*>(st + C::kCodes);
+      const float ks = *static_cast<const volatile float*>(scales + 2 * stage);
       if (key0 < lim_hi && !(ks < 0.f)) {
         // ---- S^T = K q^T
         float s[NT][4];
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
             }
         }
         // ---- the V scale as a ratio to the reference
-        const float vs = *reinterpret_cast<const volatile float*>(st + C::kCodes + 4);
+        const float vs = *static_cast<const volatile float*>(scales + 2 * stage + 1);
         if (vs > vref || (vs < vref * 0.000244140625f && vs > 0.f)) {
           const float a = vref / vs;
 #pragma unroll
@@ -639,14 +642,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
 namespace {
 template <int D, int kType, int NT>
 cudaError_t launch(const Kv8AttendParams& p, int sms, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(kWarps) * Cfg<D>::kRing + (p.B + 1) * sizeof(int);
+  const size_t smem = Cfg<D>::kPrefix + (p.B + 1) * sizeof(int);
   static std::atomic<bool> raised[64];  // this variant's shared-memory limit, by device
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !raised[dev].load(std::memory_order_acquire)) {
     cudaError_t e = cudaFuncSetAttribute(
         kv8_decode_kernel<D, kType, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>(kWarps * Cfg<D>::kRing + (kMaxRequests + 1) * sizeof(int)));
+        static_cast<int>(Cfg<D>::kPrefix + (kMaxRequests + 1) * sizeof(int)));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) raised[dev].store(true, std::memory_order_release);
   }
