@@ -124,6 +124,12 @@ __device__ __forceinline__ Request request_of(const Kv8AttendParams& p, int b, b
   return r;
 }
 
+// A unit that a CTA holds a part of.
+struct Cut {
+  int first_tile, row0, rows, kvh, q0, c0, c1;  // c0 .. c1: the CTAs with its parts
+  int last;                                     // this CTA finished last
+};
+
 }  // namespace
 
 template <int D, int kType, int NT>
@@ -137,7 +143,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
   int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);  // [B + 1] tiles before request b
   __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
   __shared__ int warp_tiles[kWarps];
-  __shared__ int s_last;
+  __shared__ Cut cuts[2];
+  int ncuts = 0;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, t4 = lane & 3;
@@ -585,58 +592,82 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
       __syncthreads();
     }
 
-    // ---- the last CTA of a cut unit joins its parts in order
+    // ---- a cut unit's parts are joined by the CTA that finishes last, once
+    // its own list is done: nobody waits for the counter here
     if (!whole) {
-      const int first_tile = at - seg - tile0, last_tile = first_tile + here.r.tiles - 1;
-      // CTA of list index x: the largest c with floor(c * total / G) <= x
-      const int c0 = static_cast<int>(((first_tile + 1ll) * G - 1) / total);
-      const int c1 = static_cast<int>(((last_tile + 1ll) * G - 1) / total);
       if (tid == 0) {
+        Cut& c = cuts[ncuts];
+        c.first_tile = at - seg - tile0;
+        c.row0 = rt * kRows;
+        c.rows = rows;
+        c.kvh = kvh;
+        c.q0 = here.r.q0;
+        // CTA of list index x: the largest c with floor(c * total / G) <= x
+        c.c0 = static_cast<int>(((c.first_tile + 1ll) * G - 1) / total);
+        c.c1 = static_cast<int>(((c.first_tile + static_cast<long long>(here.r.tiles)) * G - 1) / total);
         __threadfence();
         // a unit is cut at the end of its first CTA, and a CTA's end cuts one unit
-        s_last = atomicInc(p.counters + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+        c.last = atomicInc(p.counters + c.c0, c.c1 - c.c0) == static_cast<unsigned>(c.c1 - c.c0);
         __threadfence();
       }
-      __syncthreads();
-      if (s_last) {
-        // the unit's first part is its CTA's first segment only if the CTA begins there
-        const int begin0 = static_cast<int>(static_cast<long long>(c0) * total / G);
-        const size_t slot0 = 2 * static_cast<size_t>(c0) + (begin0 == first_tile ? 0 : 1);
-        for (int e = tid; e < rows * (D / 4); e += kThreads) {
-          const int n = e / (D / 4), d = 4 * (e % (D / 4));
-          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-          float M = -INFINITY, L = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const size_t at_part = (c == c0 ? slot0 : 2 * static_cast<size_t>(c)) * kRows + n;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at_part));
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + at_part * D + d));
-            const float mn = fmaxf(M, ml.x);
-            if (mn == -INFINITY) {  // nothing seen yet (a sum of 0), or only NaN
-              L += ml.y;
-              continue;
-            }
-            const float a = ex2_approx(M - mn), w = ex2_approx(ml.x - mn);
-            sum = make_float4(sum.x * a + y.x * w, sum.y * a + y.y * w, sum.z * a + y.z * w,
-                              sum.w * a + y.w * w);
-            L = L * a + ml.y * w;
-            M = mn;
-          }
-          const int r = rt * kRows + n, head = kvh * p.g + r % p.g;
-          const size_t token = here.r.q0 + r / p.g;
-          const float inv = L != 0.f ? 1.f / L : 0.f;
-          uint2 y;
-          y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
-          y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
-          *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
-          if (d == 0 && p.lse)
-            p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-                L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
-        }
-      }
-      __syncthreads();
+      ++ncuts;
     }
   }
   cp_wait<0>();
+
+  // ---- the joins, parts in order
+  if (ncuts > 0) __syncthreads();
+  for (int i = 0; i < ncuts; ++i) {
+    const Cut c = cuts[i];
+    if (!c.last) continue;
+    // the unit's first part is its CTA's first segment only if the CTA begins there
+    const int begin0 = static_cast<int>(static_cast<long long>(c.c0) * total / G);
+    const int slot0 = begin0 == c.first_tile ? 0 : 1;
+    for (int e = tid; e < c.rows * (D / 4); e += kThreads) {
+      const int n = e / (D / 4), d = 4 * (e % (D / 4));
+      auto part = [&](int x) { return (2 * static_cast<size_t>(x) + (x == c.c0 ? slot0 : 0)) * kRows + n; };
+      // (eight parts' loads at a time)
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float M = -INFINITY, L = 0.f;
+      for (int x0 = c.c0; x0 <= c.c1; x0 += 8) {
+        float2 ml[8];
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.f);
+          y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (x0 + j <= c.c1) {
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * part(x0 + j)));
+            y[j] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part(x0 + j) * D + d));
+          }
+        }
+        float mn = M;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) mn = fmaxf(mn, ml[j].x);
+        const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: sums of 0 (or NaN)
+        const float a = ex2_approx(M - ref);
+        sum = make_float4(sum.x * a, sum.y * a, sum.z * a, sum.w * a);
+        L = M == -INFINITY ? L : L * a;
+        M = mn;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float w = ex2_approx(ml[j].x - ref);
+          sum = make_float4(sum.x + y[j].x * w, sum.y + y[j].y * w, sum.z + y[j].z * w, sum.w + y[j].w * w);
+          L += ml[j].x == -INFINITY ? ml[j].y : ml[j].y * w;
+        }
+      }
+      const int r = c.row0 + n, head = c.kvh * p.g + r % p.g;
+      const size_t token = c.q0 + r / p.g;
+      const float inv = L != 0.f ? 1.f / L : 0.f;
+      uint2 y;
+      y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
+      y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
+      *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
+      if (d == 0 && p.lse)
+        p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
+            L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    }
+  }
 }
 
 namespace {
