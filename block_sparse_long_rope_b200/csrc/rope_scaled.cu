@@ -11,10 +11,13 @@
 // that the bound has room for (2^-25 for cos, 2^-25 for m cos, two of 2^-24 for
 // product and sum stay below 2^-22).
 //
-// Bound: HBM, 4 bytes an element. A CTA covers tpc tokens of hpc heads: it
-// issues its first loads, builds the (cos, sin) table of its tokens in shared
-// memory while they are on the way, then streams 16-byte vectors, kBatch of
-// them a thread at once.
+// Bound: HBM, 4 bytes an element. A unit is 16 elements of a head row: 8 pairs
+// (of the half layout two 16-byte vectors rot/2 apart, of the interleaved one two
+// neighbours) or 16 elements to copy. A thread keeps one unit of one token and
+// walks over heads, its 8 cosines and sines in registers; the CTA builds them
+// once in shared memory, with their fp64 values for the slow path. The rounding
+// test takes both ends of the error interval as packed bf16 pairs and branches
+// once for a unit's 8 pairs.
 #include <cmath>
 
 #include "kv8_kernels.cuh"
@@ -27,135 +30,157 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;
-constexpr int kBatch = 4;  // units of a thread in flight
+constexpr int kBatch = 2;  // heads of a thread in flight
 
-// The rare slow path, out of line: both outputs of a pair in fp64.
-__device__ __noinline__ uint32_t scaled_pair_exact(float a, float b, long long pos, double f,
-                                                   double mscale, double sign) {
-  double c, s;
-  rope_angle(pos, f, &c, &s);
-  s *= sign;
+// Both outputs of a pair in fp64 (first in the lower half), rounded once.
+__device__ __noinline__ uint32_t scaled_pair_exact(float a, float b, double c, double s) {
   const double ad = a, bd = b;
-  const uint32_t o0 = pack_bf16x2(f32_round_odd((ad * c - bd * s) * mscale), 0.f) & 0xFFFFu;
-  const uint32_t o1 = pack_bf16x2(f32_round_odd((bd * c + ad * s) * mscale), 0.f) & 0xFFFFu;
+  const uint32_t o0 = pack_bf16x2(f32_round_odd(ad * c - bd * s), 0.f) & 0xFFFFu;
+  const uint32_t o1 = pack_bf16x2(f32_round_odd(bd * c + ad * s), 0.f) & 0xFFFFu;
   return o0 | (o1 << 16);
 }
 
 }  // namespace
 
-// A unit is one thread's share of a head row: of the rotated part a 16-byte
-// vector and its partner rot/2 elements on (half), or one 16-byte vector of
-// four pairs (interleaved); of the rest one vector.
-template <bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_scaled_kernel(const __grid_constant__ RopeScaledParams p) {
-  __shared__ float2 tab[kMaxTok][64];  // m (cos, sin)
+template <int D, bool kInter>
+__global__ void __launch_bounds__(kThreads, 3) rope_scaled_kernel(const __grid_constant__ RopeScaledParams p) {
+  constexpr int kUnits = D / 16;          // threads of a head row
+  constexpr int kGroups = kThreads / kUnits;
+  __shared__ double2 exact[kMaxTok][64];  // m (cos, sin)
+  // their fp32 roundings, 8 pairs of a unit and a gap: units lie in other banks
+  __shared__ float2 tab[kMaxTok][kUnits * 10];
   const int half = p.rot / 2;
   const int tok0 = blockIdx.x * p.tpc, ntok = imin(p.tpc, p.S - tok0);
-  const int h0 = blockIdx.z * p.hpc, nh = imin(p.hpc, p.H - h0);
   const int b = blockIdx.y;
-  const unsigned rot_units = kInter ? p.rot / 8 : p.rot / 16;
-  const unsigned per_row = rot_units + (p.copy_rest ? (p.D - p.rot) / 8 : 0);
-  const unsigned per_tok = per_row * nh, units = per_tok * ntok;
-  // u / per_tok and rem / per_row by one multiply-high (u * divisor < 2^32)
-  const unsigned magic_t = 0xFFFFFFFFu / per_tok + 1u, magic_r = 0xFFFFFFFFu / per_row + 1u;
-  const __nv_bfloat16* xb = p.x + b * p.xs[0];
-  __nv_bfloat16* yb = p.y + b * p.ys[0];
+  const int u = threadIdx.x % kUnits, g = threadIdx.x / kUnits;
+  const int per = kGroups / p.tpc;        // threads that share a token's heads
+  const int t = g / per;
+  const int h_end = imin(p.H, static_cast<int>(blockIdx.z + 1) * p.hpc);
+  int h = blockIdx.z * p.hpc + g % per;
+  const bool pairs = 16 * u < p.rot;
+  const int first = !pairs ? 16 * u : kInter ? 16 * u : 8 * u;    // this unit's two vectors
+  const int second = !pairs || kInter ? first + 8 : first + half;
+  const bool mine = t < ntok && (pairs || p.copy_rest);
+  const __nv_bfloat16* x = p.x + b * p.xs[0] + (tok0 + static_cast<long long>(t)) * p.xs[1];
+  __nv_bfloat16* y = p.y + b * p.ys[0] + (tok0 + static_cast<long long>(t)) * p.ys[1];
 
   uint4 lo[kBatch], hi[kBatch];
-  int tok[kBatch], row[kBatch], unit[kBatch];
-  auto load = [&](unsigned u0) {
+  auto load = [&]() {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const unsigned u = u0 + i * kThreads;
-      if (u >= units) {
-        tok[i] = -1;
-        continue;
-      }
-      const unsigned t = per_tok == 1 ? u : __umulhi(u, magic_t);
-      const unsigned rem = u - t * per_tok;
-      const unsigned h = per_row == 1 ? rem : __umulhi(rem, magic_r);
-      tok[i] = t;
-      row[i] = h0 + h;
-      unit[i] = rem - h * per_row;
-      const __nv_bfloat16* xr = xb + (tok0 + static_cast<long long>(t)) * p.xs[1] + row[i] * p.xs[2];
-      if (unit[i] < static_cast<int>(rot_units)) {
-        lo[i] = *reinterpret_cast<const uint4*>(xr + 8 * unit[i]);
-        if (!kInter) hi[i] = *reinterpret_cast<const uint4*>(xr + half + 8 * unit[i]);
-      } else {
-        lo[i] = *reinterpret_cast<const uint4*>(xr + p.rot + 8 * (unit[i] - rot_units));
+      const int hh = h + i * per;
+      if (mine && hh < h_end) {
+        lo[i] = *reinterpret_cast<const uint4*>(x + hh * p.xs[2] + first);
+        hi[i] = *reinterpret_cast<const uint4*>(x + hh * p.xs[2] + second);
       }
     }
   };
-  load(threadIdx.x);
-
-  auto position = [&](int t) -> long long {
-    return p.pos ? p.pos[b * p.pos_stride_b + tok0 + t] : p.pos0 + tok0 + t;
-  };
+  load();
   for (int e = threadIdx.x; e < ntok * half; e += kThreads) {
-    const int t = e / half, i = e - t * half;
+    const int tt = e / half, i = e - tt * half;
+    const long long pos = p.pos ? p.pos[b * p.pos_stride_b + tok0 + tt] : p.pos0 + tok0 + tt;
     double c, s;
-    rope_angle(position(t), p.inv_freq[i], &c, &s);
-    tab[t][i] = make_float2(static_cast<float>(c * p.mscale), static_cast<float>(s * p.sign * p.mscale));
+    rope_angle(pos, p.inv_freq[i], &c, &s);
+    c *= p.mscale;
+    s *= p.sign * p.mscale;
+    exact[tt][i] = make_double2(c, s);
+    tab[tt][i + 2 * (i / 8)] = make_float2(static_cast<float>(c), static_cast<float>(s));
   }
   __syncthreads();
+  if (!mine) return;
+  float c[8], s[8];
+  if (pairs) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 v = *reinterpret_cast<const float4*>(&tab[t][10 * u + 2 * j]);
+      c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
+    }
+  }
+  const float bound = 2.3841858e-07f * p.mscale_abs;
 
-  auto pair = [&](float a, float bb, int t, int i) -> uint32_t {
-    const float2 cs = tab[t][i];
-    const float e = 2.3841858e-07f * p.mscale_abs * (fabsf(a) + fabsf(bb));
-    const float y0 = fmaf(a, cs.x, -(bb * cs.y)), y1 = fmaf(bb, cs.x, a * cs.y);
-    const uint32_t r0 = pack_bf16x2(y0 - e, y0 + e), r1 = pack_bf16x2(y1 - e, y1 + e);
-    if ((r0 & 0xFFFFu) == (r0 >> 16) && (r1 & 0xFFFFu) == (r1 >> 16))
-      return __byte_perm(r0, r1, 0x5410);
-    return scaled_pair_exact(a, bb, position(t), p.inv_freq[i], p.mscale, p.sign);
-  };
-  for (unsigned u0 = threadIdx.x; u0 < units; u0 += kBatch * kThreads) {
-    if (u0 != threadIdx.x) load(u0);
+  // Units of a row's copied part and its pairs sit in different lanes of a warp
+  while (h < h_end) {
+    uint4 cl[kBatch], ch[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) cl[i] = lo[i], ch[i] = hi[i];
+    const int h_now = h;
+    h += kBatch * per;
+    load();
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      if (tok[i] < 0) continue;
-      const int t = tok[i];
-      __nv_bfloat16* yr = yb + (tok0 + static_cast<long long>(t)) * p.ys[1] + row[i] * p.ys[2];
-      if (unit[i] >= static_cast<int>(rot_units)) {
-        *reinterpret_cast<uint4*>(yr + p.rot + 8 * (unit[i] - rot_units)) = lo[i];
-        continue;
-      }
-      const uint32_t l[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
-      uint32_t ol[4], oh[4];
-      if (kInter) {
+      const int hh = h_now + i * per;
+      if (hh >= h_end) break;
+      uint32_t* l = reinterpret_cast<uint32_t*>(&cl[i]);
+      uint32_t* r = reinterpret_cast<uint32_t*>(&ch[i]);
+      if (pairs) {
+        // pair j: elements a_j, b_j and both outputs' interval ends, packed (first,
+        // second); they agree unless a rounding boundary lies between
+        auto elem = [&](int j, float& a, float& bb) {
+          if (kInter) {
+            const uint32_t w = j < 4 ? l[j] : r[j - 4];
+            a = bf16_lo(w), bb = bf16_hi(w);
+          } else {
+            a = j & 1 ? bf16_hi(l[j >> 1]) : bf16_lo(l[j >> 1]);
+            bb = j & 1 ? bf16_hi(r[j >> 1]) : bf16_lo(r[j >> 1]);
+          }
+        };
+        uint32_t out[8], bad = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) ol[w] = pair(bf16_lo(l[w]), bf16_hi(l[w]), t, 4 * unit[i] + w);
-      } else {
-        const uint32_t r[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int i0 = 8 * unit[i] + 2 * w;
-          const uint32_t p0 = pair(bf16_lo(l[w]), bf16_lo(r[w]), t, i0);
-          const uint32_t p1 = pair(bf16_hi(l[w]), bf16_hi(r[w]), t, i0 + 1);
-          ol[w] = __byte_perm(p0, p1, 0x5410);  // first outputs of both pairs
-          oh[w] = __byte_perm(p0, p1, 0x7632);
+        for (int j = 0; j < 8; ++j) {
+          float a, bb;
+          elem(j, a, bb);
+          const float e = bound * (fabsf(a) + fabsf(bb));
+          const float y0 = fmaf(a, c[j], -(bb * s[j])), y1 = fmaf(bb, c[j], a * s[j]);
+          out[j] = pack_bf16x2(y0 - e, y1 - e);
+          if (out[j] != pack_bf16x2(y0 + e, y1 + e)) bad |= 1u << j;
         }
-        *reinterpret_cast<uint4*>(yr + half + 8 * unit[i]) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        if (bad) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (!((bad >> j) & 1u)) continue;
+            float a, bb;
+            elem(j, a, bb);
+            const double2 cs = exact[t][8 * u + j];
+            out[j] = scaled_pair_exact(a, bb, cs.x, cs.y);
+          }
+        }
+        if (kInter) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[j] = out[j], r[j] = out[4 + j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            l[j] = __byte_perm(out[2 * j], out[2 * j + 1], 0x5410);  // first outputs
+            r[j] = __byte_perm(out[2 * j], out[2 * j + 1], 0x7632);
+          }
+        }
       }
-      *reinterpret_cast<uint4*>(yr + 8 * unit[i]) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + first) = cl[i];
+      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + second) = ch[i];
     }
   }
 }
 
 cudaError_t launch_rope_scaled(const RopeScaledParams& p_in, bool interleaved, cudaStream_t stream) {
   RopeScaledParams p = p_in;
-  // 8 tokens a CTA share one table; a short call takes fewer, then fewer heads,
-  // so that its grid still covers the GPU
+  const int groups = kThreads / (p.D / 16);  // (token, head) rows of a CTA at a time
+  // 8 tokens a CTA share their table's cost; a short call takes fewer, then fewer
+  // heads, so that its grid still covers the GPU
   p.tpc = kMaxTok;
   while (p.tpc > 1 && (long long)ceil_div(p.S, p.tpc) * p.B < 2 * 148) p.tpc /= 2;
-  const int row_units = p.rot / (interleaved ? 8 : 16) + (p.copy_rest ? (p.D - p.rot) / 8 : 0);
-  // the multiply-high division needs units * divisor < 2^32: 8 * 8192 * 8192
-  p.hpc = imin(p.H, 8192 / row_units);
-  if (p.tpc == 1 && (long long)p.S * p.B < 148) p.hpc = imax(1, kThreads / row_units);
+  p.hpc = (long long)ceil_div(p.S, p.tpc) * p.B < 148 ? imin(p.H, groups / p.tpc) : p.H;
   const dim3 grid(ceil_div(p.S, p.tpc), p.B, ceil_div(p.H, p.hpc));
-  if (interleaved)
-    rope_scaled_kernel<true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    rope_scaled_kernel<false><<<grid, kThreads, 0, stream>>>(p);
+  if (p.D == 128) {
+    if (interleaved)
+      rope_scaled_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
+    else
+      rope_scaled_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
+  } else {
+    if (interleaved)
+      rope_scaled_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
+    else
+      rope_scaled_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError();
 }
 
