@@ -30,7 +30,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 8;
-constexpr int kBatch = 2;  // heads of a thread in flight
+// Heads of a thread in flight; with 64 registers, four CTAs of an SM hide the rest
+// (63.1 us for 16K tokens x 40 heads; the next heads' loads ahead of the
+// arithmetic take 80 registers, three CTAs and 65.5 us).
+constexpr int kBatch = 2;
 
 // Both outputs of a pair in fp64 (first in the lower half), rounded once.
 __device__ __noinline__ uint32_t scaled_pair_exact(float a, float b, double c, double s) {
@@ -43,7 +46,7 @@ __device__ __noinline__ uint32_t scaled_pair_exact(float a, float b, double c, d
 }  // namespace
 
 template <int D, bool kInter>
-__global__ void __launch_bounds__(kThreads, 3) rope_scaled_kernel(const __grid_constant__ RopeScaledParams p) {
+__global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_constant__ RopeScaledParams p) {
   constexpr int kUnits = D / 16;          // threads of a head row
   constexpr int kGroups = kThreads / kUnits;
   __shared__ double2 exact[kMaxTok][64];  // m (cos, sin)
@@ -100,18 +103,12 @@ __global__ void __launch_bounds__(kThreads, 3) rope_scaled_kernel(const __grid_c
 
   // Units of a row's copied part and its pairs sit in different lanes of a warp
   while (h < h_end) {
-    uint4 cl[kBatch], ch[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) cl[i] = lo[i], ch[i] = hi[i];
-    const int h_now = h;
-    h += kBatch * per;
-    load();
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int hh = h_now + i * per;
+      const int hh = h + i * per;
       if (hh >= h_end) break;
-      uint32_t* l = reinterpret_cast<uint32_t*>(&cl[i]);
-      uint32_t* r = reinterpret_cast<uint32_t*>(&ch[i]);
+      uint32_t* l = reinterpret_cast<uint32_t*>(&lo[i]);
+      uint32_t* r = reinterpret_cast<uint32_t*>(&hi[i]);
       if (pairs) {
         // pair j: elements a_j, b_j and both outputs' interval ends, packed (first,
         // second); they agree unless a rounding boundary lies between
@@ -155,9 +152,11 @@ __global__ void __launch_bounds__(kThreads, 3) rope_scaled_kernel(const __grid_c
           }
         }
       }
-      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + first) = cl[i];
-      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + second) = ch[i];
+      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + first) = lo[i];
+      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + second) = hi[i];
     }
+    h += kBatch * per;
+    load();
   }
 }
 
