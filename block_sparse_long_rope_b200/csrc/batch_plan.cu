@@ -21,7 +21,7 @@ namespace star {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 struct Sums {
@@ -171,9 +171,10 @@ cudaError_t launch_batch_plan(const BatchPlanParams& p, cudaStream_t stream) {
   cudaError_t e = set_smem_attr_once((const void*)batch_plan_kernel, 10, dev,
                                      (4 * kMaxRequests + 3) * sizeof(int));
   if (e != cudaSuccess) return e;
-  // four outputs a thread; one CTA needs no ticket
+  // An output a thread (256 requests, 12K tokens: 4.6 us; four outputs, or 512
+  // threads: 6.7 and 5.1 us). One CTA needs no ticket.
   const int most = imax(p.n_cap, p.run_cap);
-  const int grid = imax(1, imin(148, ceil_div(most, 4 * kThreads)));
+  const int grid = imax(1, imin(148, ceil_div(most, kThreads)));
   batch_plan_kernel<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
