@@ -159,9 +159,32 @@ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
-// A bounded wait with one answer for the whole warp.
+// Arrival of a warp, its lanes' writes before it.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// A bounded wait: as mbar_wait, by the SM's clock (%globaltimer takes long to
+// read, and a wait that is not over at once would read it first).
+constexpr long long kWaitClocks = 4000000000ll;  // 2 s at 2 GHz
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > kWaitClocks) {
+        atomicOr(status, kDevTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+// One answer for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+  return __all_sync(0xffffffffu, wait(bar, parity, abort, status));
 }
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   uint32_t r;
@@ -178,21 +201,43 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
 
-// The softmax's two passes over a row's 128 scores, 32 at a time from tensor
-// memory (the next 32 on their way). Loops of two such steps, not unrolled:
-// the roles of a block share small instruction caches.
-// Score j in log2 units is s_j fs ks; keys from `seen` on and keys of missing
-// pages (ks < 0) are -inf.
-template <bool kMasked>
-__device__ __forceinline__ float max_of_32(uint32_t (&s)[32], const float* ks, float fs, int seen) {
-  float mt = -INFINITY;
+// 64 columns of this thread's lane, there when it returns: a load that ends
+// later could meet the compiler's own copies of its registers.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]),
+        "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]),
+        "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]),
+        "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
+        "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]),
+        "=r"(a[30]), "=r"(a[31]),
+        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
+        "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]),
+        "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]),
+        "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
+        "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]),
+        "=r"(b[30]), "=r"(b[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Steps of the softmax over 32 of a row's scores s. Score j in log2 units is
+// s_j f, f = fs ks for the two groups of 16 keys.
+// At an edge: scaled scores, with -inf for keys from `seen` on and for those of
+// missing pages (ks < 0); f is 1 from then on.
+__device__ __forceinline__ void mask_32(uint32_t (&s)[32], const float* ks, float fs, int seen) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float k = ks[j >> 4], v = __uint_as_float(s[j]) * (fs * k);
+    s[j] = j < seen && !(k < 0.f) ? __float_as_uint(v) : 0xFF800000u;
+  }
+}
+__device__ __forceinline__ float max_32(const uint32_t (&s)[32], float f0, float f1) {
+  float m[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    if (kMasked) {
-#pragma unroll
-      for (int j = 16 * g; j < 16 * g + 16; ++j)
-        if (j >= seen || ks[g] < 0.f) s[j] = 0xFF800000u;
-    }
     const uint32_t* v = s + 16 * g;
     float a = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
     float b = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
@@ -201,49 +246,24 @@ __device__ __forceinline__ float max_of_32(uint32_t (&s)[32], const float* ks, f
       a = fmax3(a, __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
       b = fmax3(b, __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
     }
-    a = fmax3(a, b, fmaxf(__uint_as_float(v[14]), __uint_as_float(v[15])));
-    // (-inf times a scale of 0 is no number, and the maximum ignores it)
-    mt = fmaxf(mt, a * (fs * ks[g]));
+    m[g] = fmax3(a, b, fmaxf(__uint_as_float(v[14]), __uint_as_float(v[15])));
   }
-  return mt;
+  return fmaxf(m[0] * f0, m[1] * f1);
 }
-template <bool kMasked>
-__device__ __forceinline__ float row_max(uint32_t tS, const Scales& ss, float fs, int seen) {
-  uint32_t a[32], b[32];
-  float mt = -INFINITY;
-  tmem_ld32(tS, a);
-#pragma unroll 1
-  for (int q = 0; q < 4; q += 2) {
-    tmem_wait_ld();
-    reg_fence32(a);
-    tmem_ld32(tS + 32 * q + 32, b);
-    mt = fmaxf(mt, max_of_32<kMasked>(a, ss.k + 2 * q, fs, seen - 32 * q));
-    tmem_wait_ld();
-    reg_fence32(b);
-    if (q == 0) tmem_ld32(tS + 64, a);
-    mt = fmaxf(mt, max_of_32<kMasked>(b, ss.k + 2 * q + 2, fs, seen - 32 * q - 32));
-  }
-  return mt;
-}
-// P = 2^(s - rf) times the ratio of the V scale to its reference, as fp16 pairs
-// over the first half of S (columns are read before they are written);
-// returns the sum of 2^(s - rf).
-template <bool kMasked, bool kEven>
-__device__ __forceinline__ void p_of_32(const uint32_t (&s)[32], const float* ks, const float* vs, float fs,
-                                        int seen, uint64_t nref, float ivref, uint64_t (&ls)[2], uint32_t dst) {
+// P = 2^(s f - rf) times the ratio of the V scale to its reference, as fp16
+// pairs to tensor memory; ls receives the sums of 2^(s f - rf).
+template <bool kEven>
+__device__ __forceinline__ void p_32(const uint32_t (&s)[32], float f0, float f1, float r0, float r1,
+                                     uint64_t nref, uint64_t (&ls)[2], uint32_t dst) {
   uint32_t pk[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float f = fs * ks[g], ratio = kEven ? 1.f : vs[g] * ivref;
-    const uint64_t ff = f2_pack(f, f), rr = f2_pack(ratio, ratio);
+    const float f = g ? f1 : f0, r = g ? r1 : r0;
+    const uint64_t ff = f2_pack(f, f), rr = f2_pack(r, r);
 #pragma unroll
     for (int j = 8 * g; j < 8 * g + 8; ++j) {
       float x0, x1;
       f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), ff, nref), x0, x1);
-      if (kMasked) {
-        if (2 * j >= seen || ks[g] < 0.f) x0 = -INFINITY;
-        if (2 * j + 1 >= seen || ks[g] < 0.f) x1 = -INFINITY;
-      }
       uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
       ls[j & 1] = f2_add(ls[j & 1], e);
       if (!kEven) e = f2_mul(e, rr);
@@ -252,30 +272,6 @@ __device__ __forceinline__ void p_of_32(const uint32_t (&s)[32], const float* ks
     }
   }
   tmem_st16(dst, pk);
-}
-template <bool kMasked, bool kEven>
-__device__ __forceinline__ float write_p(uint32_t tS, const Scales& ss, float fs, int seen, float rf,
-                                         float ivref) {
-  uint32_t a[32], b[32];
-  const uint64_t nref = f2_pack(-rf, -rf);
-  uint64_t ls[2] = {0ull, 0ull};
-  tmem_ld32(tS, a);
-#pragma unroll 1
-  for (int q = 0; q < 4; q += 2) {
-    tmem_wait_ld();
-    reg_fence32(a);
-    tmem_ld32(tS + 32 * q + 32, b);
-    p_of_32<kMasked, kEven>(a, ss.k + 2 * q, ss.v + 2 * q, fs, seen - 32 * q, nref, ivref, ls, tS + 16 * q);
-    tmem_wait_ld();
-    reg_fence32(b);
-    if (q == 0) tmem_ld32(tS + 64, a);
-    p_of_32<kMasked, kEven>(b, ss.k + 2 * q + 2, ss.v + 2 * q + 2, fs, seen - 32 * q - 32, nref, ivref, ls,
-                            tS + 16 * q + 16);
-  }
-  float a0, a1, b0, b1;
-  f2_unpack(ls[0], a0, a1);
-  f2_unpack(ls[1], b0, b1);
-  return (a0 + a1) + (b0 + b1);
 }
 
 // Bit d of the result: a NaN code in column 32 * part + d of the V rows of keys
@@ -308,8 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   int* prefix = reinterpret_cast<int*>(sm + C::kOffPrefix);  // [B + 1] tiles before request b
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], join, done;
-  __shared__ uint64_t k_full[S], k_empty[S], v_full[S], v_empty[S], sc_full[kRing], nan_full[kRing];
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2], join;
+  __shared__ uint64_t k_full[S], v_full[S], empty[S], sc_full[kRing], nan_full[kRing];
   __shared__ __align__(16) Scales ring[kRing];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -349,23 +345,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     }
     if (tid == 0) {
       for (int x = 0; x < 2; ++x) {
-        mbar_init(&q_full[x], 128);
+        mbar_init(&q_full[x], 4);  // (by warp)
         mbar_init(&s_full[x], 1);
-        mbar_init(&p_full[x], 128);
+        mbar_init(&p_full[x], 4);
         mbar_init(&o_full[x], 1);
+        mbar_init(&done[x], 1);
       }
       for (int s = 0; s < S; ++s) {
-        mbar_init(&k_full[s], 128);
-        mbar_init(&k_empty[s], 1);
-        mbar_init(&v_full[s], 128);
-        mbar_init(&v_empty[s], 1);
+        mbar_init(&k_full[s], 4);
+        mbar_init(&v_full[s], 4);
+        mbar_init(&empty[s], 2);  // V of a tile and K of the next are free
       }
       for (int s = 0; s < kRing; ++s) {
         mbar_init(&sc_full[s], 4);
         mbar_init(&nan_full[s], 4);
       }
-      mbar_init(&join, 256);
-      mbar_init(&done, 1);
+      mbar_init(&join, 8);
       fence_barrier_init();
       abort_flag = 0;
     }
@@ -389,71 +384,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 
   if (warp >= 12) {
     // ------------------------------------------------------------ MMA issuer
-    if (warp == 12 && lane == 0) {
+    // a warp for each slot: what one does between its products runs beside the other's
+    const int x = warp - 12;
+    if (x < 2 && lane == 0) {
       constexpr uint32_t idS = idesc_f16(128, 128, 0);  // S = Q K^T, both K-major
       constexpr uint32_t idO = idesc_f16(128, D, 1);    // O += P V, V is N-major
-      const uint32_t q_lo = desc_lo(smem_u32(sm), 16), k_lo = desc_lo(smem_u32(sm) + C::kOffK, 16);
+      const uint32_t q_lo = desc_lo(smem_u32(sm) + x * C::kTile, 16), k_lo = desc_lo(smem_u32(sm) + C::kOffK, 16);
       const uint32_t v_lo = desc_lo(smem_u32(sm) + C::kOffV, C::kHalf);
+      const uint32_t tS = tmem + 128 * x, tO = tmem + 256 + 128 * x;
       // K-major operands: 16 columns are 32 bytes, 64 columns a half tile
-      auto issue_s = [&](int x, int st) {
-        const uint32_t a = q_lo + x * (C::kTile >> 4), b = k_lo + st * (C::kTile >> 4);
+      auto issue_s = [&](int st) {
+        const uint32_t b = k_lo + st * (C::kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t at = ((kk >> 2) * C::kHalf + (kk & 3) * 32) >> 4;
-          mma_ss_lo(tmem + 128 * x, a + at, b + at, idS, kk > 0 ? 1u : 0u);
+          mma_ss_lo(tS, q_lo + at, b + at, idS, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[x]);
       };
-      uint32_t cnt[2] = {0, 0};   // tiles of a slot so far
-      uint32_t segs[2] = {0, 0};  // segments of a slot so far
-      bool ok = mbar_wait(&k_full[0], 0, &abort_flag, p.status);
-      int now = ring[0].flags[0];
-      for (int x = 0; ok && x < (now & kTwo ? 2 : 1); ++x) {
-        if (!(ok = mbar_wait(&q_full[x], 0, &abort_flag, p.status))) break;
-        ++segs[x];
-        tc_fence_after();
-        issue_s(x, 0);
-      }
-      if (ok) mma_commit(&k_empty[0]);
-      for (int n = 0; ok && n < N; ++n) {
-        const int st = n % S, nst = (n + 1) % S;
+      uint32_t cnt = 0, segs = 0;  // tiles and segments of this slot so far
+      int now = 0;                 // no tile before the first
+      for (int n = -1; n < N; ++n) {
+        // products of a step: PV(n), S(n + 1)
         int next = 0;
         if (n + 1 < N) {
-          if (!mbar_wait(&k_full[nst], ((n + 1) / S) & 1, &abort_flag, p.status)) break;
+          if (!wait(&k_full[(n + 1) % S], ((n + 1) / S) & 1, &abort_flag, p.status)) break;
           next = ring[(n + 1) % kRing].flags[0];
         }
-        if (!mbar_wait(&v_full[st], (n / S) & 1, &abort_flag, p.status)) break;
+        const bool has_pv = n >= 0 && (x == 0 || (now & kTwo)), has_s = n + 1 < N && (x == 0 || (next & kTwo));
+        if (has_pv) {
+          if (!wait(&v_full[n % S], (n / S) & 1, &abort_flag, p.status)) break;
+          if (!wait(&p_full[x], cnt & 1, &abort_flag, p.status)) break;
+          ++cnt;
+          tc_fence_after();
+          const uint32_t b = v_lo + (n % S) * (C::kTile >> 4);
+          // P's keys 64 .. 127 lie in columns 64 .. 95 of S, 0 .. 63 in 96 .. 127
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (x == 0 || (now & kTwo)) {
-            if (!(ok = mbar_wait(&p_full[x], cnt[x] & 1, &abort_flag, p.status))) break;
-            ++cnt[x];
-            tc_fence_after();
-            const uint32_t b = v_lo + st * (C::kTile >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_lo(tmem + 256 + 128 * x, tmem + 128 * x + kk * 8, b + kk * (2048 >> 4), idO,
-                        (!(now & kFirst) || kk > 0) ? 1u : 0u);
-            if (now & kLast) mma_commit(&o_full[x]);
-          }
-          if (n + 1 < N && (x == 0 || (next & kTwo))) {
-            if (next & kFirst) {
-              if (!(ok = mbar_wait(&q_full[x], segs[x] & 1, &abort_flag, p.status))) break;
-              ++segs[x];
-            }
-            tc_fence_after();
-            issue_s(x, nst);
-          }
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts_lo(tO, tS + (kk < 4 ? 96 : 32) + kk * 8, b + kk * (2048 >> 4), idO,
+                      (!(now & kFirst) || kk > 0) ? 1u : 0u);
+          if (now & kLast) mma_commit(&o_full[x]);
         }
-        if (!ok) break;
-        if (n + 1 < N) mma_commit(&k_empty[nst]);
-        mma_commit(&v_empty[st]);
+        if (has_s) {
+          if (next & kFirst) {
+            if (!wait(&q_full[x], segs & 1, &abort_flag, p.status)) break;
+            ++segs;
+          }
+          tc_fence_after();
+          issue_s((n + 1) % S);
+        }
+        // both slots' arrivals free V(n) and K(n + 1). (A slot without rows keeps
+        // in step by its waits for K; nobody waits for the last step.)
+        if (n + 1 < N) {
+          if (has_pv || has_s) mma_commit(&empty[(n + 1) % S]);
+          else mbar_arrive(&empty[(n + 1) % S]);
+        }
         now = next;
       }
       // every MMA in flight ends before tensor memory is released
-      mma_commit(&done);
+      mma_commit(&done[x]);
       const uint64_t t0 = global_ns();
-      while (!mbar_try_wait(&done, 0))
+      while (!mbar_try_wait(&done[x], 0))
         if (global_ns() - t0 > 100000000ull) break;
     }
     __syncwarp();
@@ -462,7 +453,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     constexpr int kLoads = D / 16;      // 16-byte loads of a thread for a K or V tile
     constexpr int kPerRow = D / 16;     // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kPerRow;
-    const int cw = warp - 8, ch = lane % kPerRow, rl = lane / kPerRow, r0 = 32 * cw + rl;
+    // At D 128 eight lanes cover a row's 128 bytes and write two 64-column halves,
+    // which lie in the same banks: the second half's lanes take the next row, whose
+    // chunks the swizzle puts elsewhere
+    const int cw = warp - 8, ch = lane % kPerRow, rl = (lane / kPerRow) ^ (ch >> 2), r0 = 32 * cw + rl;
     const int P = 1 << p.page_shift;
     struct Tile {
       int key0, left, kvh, edge, flags, page[2];  // pages of this warp's two groups of 16 keys
@@ -525,26 +519,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       if (16 * (lane & 1) >= t.left) return 0.f;
       return __ldg((lane < 2 ? p.k_scale : p.v_scale) + static_cast<size_t>(page) * p.Hkv + t.kvh);
     };
-    // Columns 16 ch .. + 15 of a row are chunks c and c + 1 of a 64-column half.
-    // At D 128 eight lanes share a row and two of them a chunk position: the
-    // second half's lanes write in the other order, so the banks differ. Rows of
-    // a thread are 4 apart (8 at D 64), so the swizzle takes two values (one).
-    const bool turn = ch >= 4;
+    // Columns 16 ch .. + 15 of a row are two chunks of a 64-column half. Rows of a
+    // thread are 4 apart (8 at D 64), so the swizzle takes two values (one).
     uint32_t at[2][2];
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        at[o][c] = (ch >> 2) * C::kHalf + sw128_offset(r0 + kRowsPer * o, ((2 * ch) & 7) + (c ^ (turn ? 1 : 0))) -
-                   128 * kRowsPer * o;
+        at[o][c] = (ch >> 2) * C::kHalf + sw128_offset(r0 + kRowsPer * o, ((2 * ch) & 7) + c) - 128 * kRowsPer * o;
     auto convert = [&](const uint4 (&x)[kLoads], uint8_t* dst) {
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         uint4 a, b;
-        codes_to_half2<kType>(turn ? x[j].z : x[j].x, a.x, a.y);
-        codes_to_half2<kType>(turn ? x[j].w : x[j].y, a.z, a.w);
-        codes_to_half2<kType>(turn ? x[j].x : x[j].z, b.x, b.y);
-        codes_to_half2<kType>(turn ? x[j].y : x[j].w, b.z, b.w);
+        codes_to_half2<kType>(x[j].x, a.x, a.y);
+        codes_to_half2<kType>(x[j].y, a.z, a.w);
+        codes_to_half2<kType>(x[j].z, b.x, b.y);
+        codes_to_half2<kType>(x[j].w, b.z, b.w);
         *reinterpret_cast<uint4*>(dst + at[j & 1][0] + 128 * kRowsPer * j) = a;
         *reinterpret_cast<uint4*>(dst + at[j & 1][1] + 128 * kRowsPer * j) = b;
       }
@@ -560,24 +550,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     }
     for (int n = 0; n < N; ++n) {
       const int st = n % S;
-      const uint32_t again = ((n / S) - 1) & 1;
       // the scales' ring is deeper than the stages ahead: no wait
       Scales& ss = ring[n % kRing];
-      if (n >= S && !warp_wait(&k_empty[st], again, &abort_flag, p.status)) break;
+      if (n >= S && !warp_wait(&empty[st], (n / S - 1) & 1, &abort_flag, p.status)) break;
       if (lane < 2) ss.k[2 * cw + lane] = sc;
       else if (lane < 4) ss.v[2 * cw + lane - 2] = sc;
       else if (lane == 4) ss.nan[cw] = 0;
       else if (cw == 0 && lane == 5) ss.flags[0] = cur.flags;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sc_full[n % kRing]);
+      warp_arrive(&sc_full[n % kRing]);
       convert(kx, sm + C::kOffK + st * C::kTile);
       fence_async_shared();
-      mbar_arrive(&k_full[st]);
+      warp_arrive(&k_full[st]);
       if (n + 1 < N) {
         load(kx, nxt, p.k_pages);
         sc = load_scale(nxt);
       }
-      if (n >= S && !warp_wait(&v_empty[st], again, &abort_flag, p.status)) break;
+      if (n >= S && !warp_wait(&empty[(n + 1) % S], ((n + 1) / S - 1) & 1, &abort_flag, p.status)) break;
       if (kType == STAR_KV8_E4M3 && cur.edge) {
         // a NaN must not meet the weight 0 of rows that do not see its key: it
         // goes in as 0 and the rows that see it are told
@@ -593,14 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
         }
         if (any) ss.nan[cw] = 1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&nan_full[n % kRing]);
+        warp_arrive(&nan_full[n % kRing]);
       } else if (lane == 0) {
         mbar_arrive(&nan_full[n % kRing]);
       }
       convert(vx, sm + C::kOffV + st * C::kTile);
       fence_async_shared();
-      mbar_arrive(&v_full[st]);
+      warp_arrive(&v_full[st]);
       cur = nxt;
       if (n + 1 < N) load(vx, nxt, p.v_pages);
       if (n + 2 < N) {
@@ -616,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     uint32_t cnt = 0, segs = 0, joins = 0;
     // every softmax thread has got here (bounded)
     auto softmax_sync = [&]() {
-      mbar_arrive(&join);
+      warp_arrive(&join);
       return warp_wait(&join, joins++ & 1, &abort_flag, p.status);
     };
     float fs = 0.f;  // this row's factor: 2^-e log2(e) / sqrt(D)
@@ -648,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kHalf + sw128_offset(row, i & 7)) =
             make_uint4(two(v[i].x), two(v[i].y), two(v[i].z), two(v[i].w));
       fence_async_shared();
-      mbar_arrive(&q_full[x]);
+      warp_arrive(&q_full[x]);
     };
     Walk w = walk_to(p, prefix, begin);
     if (x == 0 || rows_of(p, w.r, w.rt) > 128) load_q(w);
@@ -666,13 +653,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
       float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f;
       bool nan = false;
+      // (a slot without rows still follows the ring: its next wait would otherwise
+      // mistake an earlier round for its own)
+      for (int i = 0; !active && ok && i < seg; ++i)
+        ok = warp_wait(&sc_full[(n0 + i) % kRing], ((n0 + i) / kRing) & 1, &abort_flag, p.status);
       for (int i = 0; active && i < seg; ++i, ++cnt) {
         const int n = n0 + i;
         const Scales& ss = ring[n % kRing];
-        if (!(ok = warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status))) break;
-        // (S of tile n is there, so its scales' phase is the last one completed)
         if (!(ok = warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
-        tc_fence_after();
         const int key0 = (here.tile + i) * kKv8Tile, seen = limit - key0;
         float kmin = ss.k[0], vmax = ss.v[0], vmin = vmax;
 #pragma unroll
@@ -681,52 +669,96 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           vmax = fmaxf(vmax, ss.v[j]);
           vmin = fminf(vmin, ss.v[j]);
         }
-        // masked keys and keys of missing pages are -inf
         const bool masked = key0 + kKv8Tile > lim_lo || kmin < 0.f;
+        const bool new_vref = vmax > vref || (vmax < vref * 0.000244140625f && vmax > 0.f);
+        auto factor = [&](int g) { return masked ? 1.f : fs * ss.k[g]; };
+
+        if (!(ok = warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status))) break;
+        tc_fence_after();
+        // ---- row maximum in log2 units, 64 scores at a time; the last 64 stay
+        // (loops that are not unrolled: the roles share small instruction caches)
+        uint32_t a[32], b[32];
+        float mt = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < 4; q += 2) {
+          tmem_ld64(tS + 32 * q, a, b);
+          if (masked) {
+            mask_32(a, ss.k + 2 * q, fs, seen - 32 * q);
+            mask_32(b, ss.k + 2 * q + 2, fs, seen - 32 * q - 32);
+          }
+          mt = fmaxf(mt, max_32(a, factor(2 * q), factor(2 * q + 1)));
+          mt = fmaxf(mt, max_32(b, factor(2 * q + 2), factor(2 * q + 3)));
+        }
         if (kType == STAR_KV8_E4M3 && key0 + kKv8Tile > unit_lo) {
           if (!(ok = warp_wait(&nan_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
           const int4 flags = *reinterpret_cast<const int4*>(ss.nan);
           nan |= (flags.x | flags.y | flags.z | flags.w) != 0;
         }
-        // ---- row maximum in log2 units
-        const float mt = masked ? row_max<true>(tS, ss, fs, seen) : row_max<false>(tS, ss, fs, seen);
-        // ---- move the maximum and the V reference; O and the sum follow
-        float alpha = 1.f;
-        if (mt > m + kSlack) {
-          m = mt;
-          // P = 2^(s - rf); where m is so large that m - 11 is rounded, rf = m
-          float nrf = m - kShift;
-          if (m - nrf > kShift) nrf = m;
-          alpha = l == 0.f ? 1.f : ex2_approx(rf - nrf);
-          rf = nrf;
-        }
-        l *= alpha;
-        if (vmax > vref || (vmax < vref * 0.000244140625f && vmax > 0.f)) {
-          alpha *= vref / vmax;
-          vref = vmax;
-          ivref = 1.f / vmax;
-        }
-        if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
-            uint32_t r[16];
-            tmem_ld16(tO + 16 * q, r);
-            tmem_wait_ld();
-            reg_fence16(r);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
-            tmem_st16(tO + 16 * q, r);
+        // ---- now and then the maximum and the V reference move; O and the sum follow
+        const bool up = mt > m + kSlack;
+        if (new_vref || __any_sync(0xffffffffu, up)) {
+          float alpha = 1.f;
+          if (up) {
+            m = mt;
+            // P = 2^(s - rf); where m is so large that m - 11 is rounded, rf = m
+            float nrf = m - kShift;
+            if (m - nrf > kShift) nrf = m;
+            alpha = l == 0.f ? 1.f : ex2_approx(rf - nrf);
+            rf = nrf;
           }
-          tmem_wait_st();
+          l *= alpha;
+          if (new_vref) {
+            alpha *= vref / vmax;
+            vref = vmax;
+            ivref = 1.f / vmax;
+          }
+          if (i > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t r[16];
+              tmem_ld16(tO + 16 * q, r);
+              tmem_wait_ld();
+              reg_fence16(r);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * alpha);
+              tmem_st16(tO + 16 * q, r);
+            }
+            tmem_wait_st();
+          }
         }
-        // ---- P, and the row's sum
+        // ---- P over the second half of S: the 64 scores at hand first, into the
+        // columns that they came from
         const bool even = vmin == vref && vmax == vref;  // every V ratio is 1
-        l += masked ? write_p<true, false>(tS, ss, fs, seen, rf, ivref)
-             : even ? write_p<false, true>(tS, ss, fs, seen, rf, ivref)
-                    : write_p<false, false>(tS, ss, fs, seen, rf, ivref);
+        const uint64_t nref = f2_pack(-rf, -rf);
+        uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          const int g = h ? 0 : 4;  // groups of 16 keys from here on
+          const uint32_t dst = tS + 64 + 32 * h;
+          if (h) {
+            tmem_ld64(tS, a, b);
+            if (masked) {
+              mask_32(a, ss.k, fs, seen);
+              mask_32(b, ss.k + 2, fs, seen - 32);
+            }
+          }
+          const float r0 = ss.v[g] * ivref, r1 = ss.v[g + 1] * ivref;
+          const float r2 = ss.v[g + 2] * ivref, r3 = ss.v[g + 3] * ivref;
+          if (even) {
+            p_32<true>(a, factor(g), factor(g + 1), r0, r1, nref, ls, dst);
+            p_32<true>(b, factor(g + 2), factor(g + 3), r2, r3, nref, ls, dst + 16);
+          } else {
+            p_32<false>(a, factor(g), factor(g + 1), r0, r1, nref, ls, dst);
+            p_32<false>(b, factor(g + 2), factor(g + 3), r2, r3, nref, ls, dst + 16);
+          }
+        }
+        float a0, a1, b0, b1;
+        f2_unpack(ls[0], a0, a1);
+        f2_unpack(ls[1], b0, b1);
+        l += (a0 + a1) + (b0 + b1);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&p_full[x]);
+        warp_arrive(&p_full[x]);
       }
       if (!ok) break;
       // ---- the next unit's rows of q while the last products run
