@@ -35,7 +35,9 @@ namespace star {
 
 namespace {
 
-constexpr int kThreads = 512;  // 2 x 4 softmax warps, 4 converter warps, 1 MMA warp (+ 3 idle)
+// Warps 0-15: softmax (slot = warp / 8, half of the keys = warp / 4 % 2), 16-19:
+// converters, 20 and 21: MMA (+ 2 idle).
+constexpr int kThreads = 768;
 constexpr int kRows = kKv8ChunkRows;
 constexpr int kRing = 8;       // tiles whose scales are kept: more than the stages ahead
 constexpr float kShift = 11.f; // P is held as 2^11 e^(s - m)
@@ -182,6 +184,14 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile in
     }
   }
 }
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // One answer for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   return __all_sync(0xffffffffu, wait(bar, parity, abort, status));
@@ -201,24 +211,18 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return __vcmpeq4(w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
 }
 
-// 64 columns of this thread's lane, there when it returns: a load that ends
+// 32 columns of this thread's lane, there when it returns: a load that ends
 // later could meet the compiler's own copies of its registers.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&a)[32], uint32_t (&b)[32]) {
+__device__ __forceinline__ void tmem_ld32_now(uint32_t taddr, uint32_t (&s)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]),
-        "=r"(a[6]), "=r"(a[7]), "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]),
-        "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]), "=r"(a[17]),
-        "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]),
-        "=r"(a[24]), "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]),
-        "=r"(a[30]), "=r"(a[31]),
-        "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
-        "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]),
-        "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]),
-        "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]),
-        "=r"(b[24]), "=r"(b[25]), "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]),
-        "=r"(b[30]), "=r"(b[31])
+      : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]),
+        "=r"(s[6]), "=r"(s[7]), "=r"(s[8]), "=r"(s[9]), "=r"(s[10]), "=r"(s[11]),
+        "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15]), "=r"(s[16]), "=r"(s[17]),
+        "=r"(s[18]), "=r"(s[19]), "=r"(s[20]), "=r"(s[21]), "=r"(s[22]), "=r"(s[23]),
+        "=r"(s[24]), "=r"(s[25]), "=r"(s[26]), "=r"(s[27]), "=r"(s[28]), "=r"(s[29]),
+        "=r"(s[30]), "=r"(s[31])
       : "r"(taddr)
       : "memory");
 }
@@ -252,7 +256,6 @@ __device__ __forceinline__ float max_32(const uint32_t (&s)[32], float f0, float
 }
 // P = 2^(s f - rf) times the ratio of the V scale to its reference, as fp16
 // pairs to tensor memory; ls receives the sums of 2^(s f - rf).
-template <bool kEven>
 __device__ __forceinline__ void p_32(const uint32_t (&s)[32], float f0, float f1, float r0, float r1,
                                      uint64_t nref, uint64_t (&ls)[2], uint32_t dst) {
   uint32_t pk[16];
@@ -264,10 +267,9 @@ __device__ __forceinline__ void p_32(const uint32_t (&s)[32], float f0, float f1
     for (int j = 8 * g; j < 8 * g + 8; ++j) {
       float x0, x1;
       f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), ff, nref), x0, x1);
-      uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
+      const uint64_t e = f2_pack(ex2_approx(x0), ex2_approx(x1));
       ls[j & 1] = f2_add(ls[j & 1], e);
-      if (!kEven) e = f2_mul(e, rr);
-      f2_unpack(e, x0, x1);
+      f2_unpack(f2_mul(e, rr), x0, x1);
       pk[j] = half2_of(x0, x1);
     }
   }
@@ -305,11 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
                                            ~static_cast<uintptr_t>(1023));
   int* prefix = reinterpret_cast<int*>(sm + C::kOffPrefix);  // [B + 1] tiles before request b
   __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2], join;
-  __shared__ uint64_t k_full[S], v_full[S], empty[S], sc_full[kRing], nan_full[kRing];
+  __shared__ uint64_t k_full[S], v_full[S], empty[S], sc_full[kRing], nan_full[kRing], lead[kRing];
   __shared__ __align__(16) Scales ring[kRing];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int s_last;
+  __shared__ float row_fs[2][128], row_l[2][2][128], row_m[2][2][2][128];  // what a row's two threads exchange
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       for (int x = 0; x < 2; ++x) {
         mbar_init(&q_full[x], 4);  // (by warp)
         mbar_init(&s_full[x], 1);
-        mbar_init(&p_full[x], 4);
+        mbar_init(&p_full[x], 8);
         mbar_init(&o_full[x], 1);
         mbar_init(&done[x], 1);
       }
@@ -359,8 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       for (int s = 0; s < kRing; ++s) {
         mbar_init(&sc_full[s], 4);
         mbar_init(&nan_full[s], 4);
+        mbar_init(&lead[s], 1);
       }
-      mbar_init(&join, 8);
+      mbar_init(&join, 16);
       fence_barrier_init();
       abort_flag = 0;
     }
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   const int end = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * total / G);
   const int N = end - begin;
 
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc(&tmem_slot, 512);
     tmem_relinquish();
   }
@@ -382,10 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  if (warp >= 12) {
+  if (warp >= 20) {
     // ------------------------------------------------------------ MMA issuer
     // a warp for each slot: what one does between its products runs beside the other's
-    const int x = warp - 12;
+    regs_down<56>();
+    const int x = warp - 20;
     if (x < 2 && lane == 0) {
       constexpr uint32_t idS = idesc_f16(128, 128, 0);  // S = Q K^T, both K-major
       constexpr uint32_t idO = idesc_f16(128, D, 1);    // O += P V, V is N-major
@@ -411,17 +416,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           if (!wait(&k_full[(n + 1) % S], ((n + 1) / S) & 1, &abort_flag, p.status)) break;
           next = ring[(n + 1) % kRing].flags[0];
         }
+        // slot 1's products come after slot 0's of the same step: one slot's softmax
+        // then runs beside the other's products, and not beside its softmax
         const bool has_pv = n >= 0 && (x == 0 || (now & kTwo)), has_s = n + 1 < N && (x == 0 || (next & kTwo));
         if (has_pv) {
           if (!wait(&v_full[n % S], (n / S) & 1, &abort_flag, p.status)) break;
           if (!wait(&p_full[x], cnt & 1, &abort_flag, p.status)) break;
           ++cnt;
+          if (x == 1 && !wait(&lead[(n + 1) % kRing], ((n + 1) / kRing) & 1, &abort_flag, p.status)) break;
           tc_fence_after();
           const uint32_t b = v_lo + (n % S) * (C::kTile >> 4);
-          // P's keys 64 .. 127 lie in columns 64 .. 95 of S, 0 .. 63 in 96 .. 127
+          // each half's P lies in the upper half of its 64 columns of S, its second 32
+          // keys first
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts_lo(tO, tS + (kk < 4 ? 96 : 32) + kk * 8, b + kk * (2048 >> 4), idO,
+            mma_ts_lo(tO, tS + 64 * (kk >> 2) + ((kk & 2) ? 16 : 48) + 8 * (kk & 3), b + kk * (2048 >> 4), idO,
                       (!(now & kFirst) || kk > 0) ? 1u : 0u);
           if (now & kLast) mma_commit(&o_full[x]);
         }
@@ -430,9 +439,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
             if (!wait(&q_full[x], segs & 1, &abort_flag, p.status)) break;
             ++segs;
           }
+          if (x == 1 && !wait(&lead[(n + 1) % kRing], ((n + 1) / kRing) & 1, &abort_flag, p.status)) break;
           tc_fence_after();
           issue_s((n + 1) % S);
         }
+        if (x == 0) mbar_arrive(&lead[(n + 1) % kRing]);
         // both slots' arrivals free V(n) and K(n + 1). (A slot without rows keeps
         // in step by its waits for K; nobody waits for the last step.)
         if (n + 1 < N) {
@@ -448,15 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         if (global_ns() - t0 > 100000000ull) break;
     }
     __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp >= 16) {
     // ------------------------------------------------------------ converters
+    regs_up<104>();  // with the MMA warps' 56: what the block was launched with
     constexpr int kLoads = D / 16;      // 16-byte loads of a thread for a K or V tile
     constexpr int kPerRow = D / 16;     // 16-byte pieces of a row
     constexpr int kRowsPer = 32 / kPerRow;
     // At D 128 eight lanes cover a row's 128 bytes and write two 64-column halves,
     // which lie in the same banks: the second half's lanes take the next row, whose
     // chunks the swizzle puts elsewhere
-    const int cw = warp - 8, ch = lane % kPerRow, rl = (lane / kPerRow) ^ (ch >> 2), r0 = 32 * cw + rl;
+    const int cw = warp - 16, ch = lane % kPerRow, rl = (lane / kPerRow) ^ (ch >> 2), r0 = 32 * cw + rl;
     const int P = 1 << p.page_shift;
     struct Tile {
       int key0, left, kvh, edge, flags, page[2];  // pages of this warp's two groups of 16 keys
@@ -597,49 +609,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int x = warp >> 2, row = tid & 127;
+    // Two threads a row: each takes 64 of a tile's 128 keys and half of O. They meet
+    // at a named barrier of their two warps; nobody leaves the loops early (an
+    // abort only makes the waits short), so every barrier is met by both.
+    const int x = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + 128 * x, tO = tmem + lanes + 256 + 128 * x;
+    const uint32_t tS = tmem + lanes + 128 * x + 64 * half, tO = tmem + lanes + 256 + 128 * x;
+    const int pair = 1 + 4 * x + (warp & 3);
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     uint32_t cnt = 0, segs = 0, joins = 0;
+    bool ok = true;
     // every softmax thread has got here (bounded)
     auto softmax_sync = [&]() {
       warp_arrive(&join);
-      return warp_wait(&join, joins++ & 1, &abort_flag, p.status);
+      ok &= warp_wait(&join, joins++ & 1, &abort_flag, p.status);
     };
-    float fs = 0.f;  // this row's factor: 2^-e log2(e) / sqrt(D)
-    // this thread's row of q into the slot's tile, as fp16 times a power of two
+    // a row of q into the slot's tile, as fp16 times a power of two
     auto load_q = [&](const Walk& w) {
+      if (half != 0 || (x == 1 && rows_of(p, w.r, w.rt) <= 128)) return;
       const int r = w.rt * kRows + 128 * x + row;
+      const bool real = r < w.r.T * p.g;
       uint8_t* dst = sm + x * C::kTile;
-      uint4 v[D / 8];
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < w.r.T * p.g) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (w.r.q0 + r / p.g) * p.qs[0] + (w.kvh * p.g + r % p.g) * p.qs[1]);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
-      }
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (w.r.q0 + (real ? r / p.g : 0)) * p.qs[0] + (w.kvh * p.g + (real ? r % p.g : 0)) * p.qs[1]);
       uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+      if (real)
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = __ldg(src + i);
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
       const int e = static_cast<int>(imax(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent
       const int up = imin(254, imax(1, 127 + 14 - (e - 127)));  // 2^(14 - (e - 127)), a normal number
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-      fs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
+      // this row's factor: 2^-e log2(e) / sqrt(D)
+      row_fs[x][row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
       auto two = [&](uint32_t u) { return half2_of(bf16_lo(u) * mul, bf16_hi(u) * mul); };
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (real) v = __ldg(src + i);
         *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kHalf + sw128_offset(row, i & 7)) =
-            make_uint4(two(v[i].x), two(v[i].y), two(v[i].z), two(v[i].w));
+            make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+      }
       fence_async_shared();
       warp_arrive(&q_full[x]);
     };
     Walk w = walk_to(p, prefix, begin);
-    if (x == 0 || rows_of(p, w.r, w.rt) > 128) load_q(w);
-    bool ok = true;
+    load_q(w);
     for (int n0 = 0; n0 < N;) {
       // ---- one segment: the tiles of one unit that this CTA holds
       const Walk here = w;
@@ -651,46 +669,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // keys that the slot's and the unit's first rows see
       const int lim_lo = keys_of_row(p, here.r, here.rt * kRows + 128 * x);
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
-      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f;
+      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f, fs = 0.f;
       bool nan = false;
-      // (a slot without rows still follows the ring: its next wait would otherwise
-      // mistake an earlier round for its own)
-      for (int i = 0; !active && ok && i < seg; ++i)
-        ok = warp_wait(&sc_full[(n0 + i) % kRing], ((n0 + i) / kRing) & 1, &abort_flag, p.status);
-      for (int i = 0; active && i < seg; ++i, ++cnt) {
+      if (active) {
+        pair_sync();
+        fs = row_fs[x][row];
+      }
+      for (int i = 0; i < seg; ++i) {
         const int n = n0 + i;
         const Scales& ss = ring[n % kRing];
-        if (!(ok = warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
-        const int key0 = (here.tile + i) * kKv8Tile, seen = limit - key0;
-        float kmin = ss.k[0], vmax = ss.v[0], vmin = vmax;
+        // (a slot without rows still follows the ring: its next wait would otherwise
+        // mistake an earlier round for its own)
+        ok &= warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status);
+        if (!active) continue;
+        const int key0 = (here.tile + i) * kKv8Tile, seen = limit - key0 - 64 * half;
+        float kmin = ss.k[0], vmax = ss.v[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) {
           kmin = fminf(kmin, ss.k[j]);
           vmax = fmaxf(vmax, ss.v[j]);
-          vmin = fminf(vmin, ss.v[j]);
         }
         const bool masked = key0 + kKv8Tile > lim_lo || kmin < 0.f;
         const bool new_vref = vmax > vref || (vmax < vref * 0.000244140625f && vmax > 0.f);
-        auto factor = [&](int g) { return masked ? 1.f : fs * ss.k[g]; };
+        const float *ks = ss.k + 4 * half, *vs = ss.v + 4 * half;
+        auto factor = [&](int g) { return masked ? 1.f : fs * ks[g]; };
 
-        if (!(ok = warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status))) break;
+        ok &= warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status);
         tc_fence_after();
-        // ---- row maximum in log2 units, 64 scores at a time; the last 64 stay
-        // (loops that are not unrolled: the roles share small instruction caches)
-        uint32_t a[32], b[32];
+        // ---- row maximum in log2 units, 32 scores at a time; the last 32 stay (loops
+        // that are not unrolled: the roles share small instruction caches)
+        uint32_t s[32];
         float mt = -INFINITY;
 #pragma unroll 1
-        for (int q = 0; q < 4; q += 2) {
-          tmem_ld64(tS + 32 * q, a, b);
-          if (masked) {
-            mask_32(a, ss.k + 2 * q, fs, seen - 32 * q);
-            mask_32(b, ss.k + 2 * q + 2, fs, seen - 32 * q - 32);
-          }
-          mt = fmaxf(mt, max_32(a, factor(2 * q), factor(2 * q + 1)));
-          mt = fmaxf(mt, max_32(b, factor(2 * q + 2), factor(2 * q + 3)));
+        for (int q = 0; q < 2; ++q) {
+          tmem_ld32_now(tS + 32 * q, s);
+          if (masked) mask_32(s, ks + 2 * q, fs, seen - 32 * q);
+          mt = fmaxf(mt, max_32(s, factor(2 * q), factor(2 * q + 1)));
         }
+        row_m[cnt & 1][x][half][row] = mt;
+        pair_sync();
+        mt = fmaxf(mt, row_m[cnt & 1][x][half ^ 1][row]);
+        ++cnt;
         if (kType == STAR_KV8_E4M3 && key0 + kKv8Tile > unit_lo) {
-          if (!(ok = warp_wait(&nan_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status))) break;
+          ok &= warp_wait(&nan_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status);
           const int4 flags = *reinterpret_cast<const int4*>(ss.nan);
           nan |= (flags.x | flags.y | flags.z | flags.w) != 0;
         }
@@ -699,11 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         if (new_vref || __any_sync(0xffffffffu, up)) {
           float alpha = 1.f;
           if (up) {
+            const bool none = m == -INFINITY;  // nothing seen so far
             m = mt;
             // P = 2^(s - rf); where m is so large that m - 11 is rounded, rf = m
             float nrf = m - kShift;
             if (m - nrf > kShift) nrf = m;
-            alpha = l == 0.f ? 1.f : ex2_approx(rf - nrf);
+            alpha = none ? 1.f : ex2_approx(rf - nrf);
             rf = nrf;
           }
           l *= alpha;
@@ -714,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
           if (i > 0) {
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
+            for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
               uint32_t r[16];
               tmem_ld16(tO + 16 * q, r);
               tmem_wait_ld();
@@ -726,31 +748,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
             tmem_wait_st();
           }
         }
-        // ---- P over the second half of S: the 64 scores at hand first, into the
-        // columns that they came from
-        const bool even = vmin == vref && vmax == vref;  // every V ratio is 1
+        // ---- P over S: the 32 scores at hand into the columns that they came from,
+        // then the others
         const uint64_t nref = f2_pack(-rf, -rf);
         uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          const int g = h ? 0 : 4;  // groups of 16 keys from here on
-          const uint32_t dst = tS + 64 + 32 * h;
-          if (h) {
-            tmem_ld64(tS, a, b);
-            if (masked) {
-              mask_32(a, ss.k, fs, seen);
-              mask_32(b, ss.k + 2, fs, seen - 32);
-            }
+        for (int q = 1; q >= 0; --q) {
+          if (q == 0) {
+            tmem_ld32_now(tS, s);
+            if (masked) mask_32(s, ks, fs, seen);
           }
-          const float r0 = ss.v[g] * ivref, r1 = ss.v[g + 1] * ivref;
-          const float r2 = ss.v[g + 2] * ivref, r3 = ss.v[g + 3] * ivref;
-          if (even) {
-            p_32<true>(a, factor(g), factor(g + 1), r0, r1, nref, ls, dst);
-            p_32<true>(b, factor(g + 2), factor(g + 3), r2, r3, nref, ls, dst + 16);
-          } else {
-            p_32<false>(a, factor(g), factor(g + 1), r0, r1, nref, ls, dst);
-            p_32<false>(b, factor(g + 2), factor(g + 3), r2, r3, nref, ls, dst + 16);
-          }
+          const float f0 = factor(2 * q), f1 = factor(2 * q + 1);
+          const uint32_t dst = tS + (q ? 32 : 48);
+          p_32(s, f0, f1, vs[2 * q] * ivref, vs[2 * q + 1] * ivref, nref, ls, dst);
         }
         float a0, a1, b0, b1;
         f2_unpack(ls[0], a0, a1);
@@ -760,31 +770,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         tc_fence_before();
         warp_arrive(&p_full[x]);
       }
-      if (!ok) break;
       // ---- the next unit's rows of q while the last products run
       n0 += seg;
       if (n0 < N) {
         next_unit(p, prefix, w, begin + n0);
-        if (x == 0 || rows_of(p, w.r, w.rt) > 128) load_q(w);
+        load_q(w);
       }
       // ---- epilogue
       const bool whole = seg == here.tiles;
       // parts of a unit: a CTA's first segment goes to slot 0, a later one to 1
       const size_t part = 2 * static_cast<size_t>(blockIdx.x) + (n0 == seg ? 0 : 1);
       if (active) {
-        if (!(ok = warp_wait(&o_full[x], segs & 1, &abort_flag, p.status))) break;
+        row_l[x][half][row] = l;
+        pair_sync();
+        l += row_l[x][half ^ 1][row];
+        ok &= warp_wait(&o_full[x], segs & 1, &abort_flag, p.status);
         ++segs;
         tc_fence_after();
-        const bool valid = 128 * x + row < rows;
+        const bool valid = ok && 128 * x + row < rows;
         const int head = here.kvh * p.g + my_row % p.g;
         const size_t token = here.r.q0 + my_row / p.g;
         const float mul = whole ? (l != 0.f ? vref / l : 0.f) : vref;
-        for (int q = 0; q < D / 32; ++q) {
+        for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {
           uint32_t r[32];
           __syncwarp();
-          tmem_ld32(tO + 32 * q, r);
-          tmem_wait_ld();
-          reg_fence32(r);
+          tmem_ld32_now(tO + 32 * q, r);
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * mul);
           if (!valid) continue;
@@ -815,10 +825,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
                                    __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
           }
         }
-        if (valid && whole && p.lse)
+        if (valid && whole && half == 0 && p.lse)
           p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
               l != 0.f ? (rf + log2f(l)) * 0.6931471805599453f : -INFINITY;
-        if (valid && !whole)  // nothing seen (or only NaN): a reference of -inf
+        if (valid && !whole && half == 0)  // nothing seen (or only NaN): a reference of -inf
           *reinterpret_cast<float2*>(p.part_ml + 2 * (part * kRows + 128 * x + row)) =
               make_float2(m == -INFINITY ? -INFINITY : rf, l);
         tc_fence_before();
@@ -828,17 +838,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         const int first_tile = begin + n0 - seg - here.tile, last_tile = first_tile + here.tiles - 1;
         const int c0 = static_cast<int>(((first_tile + 1ll) * G - 1) / total);
         const int c1 = static_cast<int>(((last_tile + 1ll) * G - 1) / total);
-        if (!(ok = softmax_sync())) break;
-        if (tid == 0) {
+        softmax_sync();
+        if (tid == 0 && ok) {
           __threadfence();
           s_last = atomicInc(p.counters + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
           __threadfence();
         }
-        if (!(ok = softmax_sync())) break;
-        if (s_last) {
+        softmax_sync();
+        if (ok && s_last) {
           const int begin0 = static_cast<int>(static_cast<long long>(c0) * total / G);
           const size_t slot0 = 2 * static_cast<size_t>(c0) + (begin0 == first_tile ? 0 : 1);
-          for (int e = tid; e < rows * (D / 4); e += 256) {
+          for (int e = tid; e < rows * (D / 4); e += 512) {
             const int r = e / (D / 4), d = 4 * (e % (D / 4));
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             float M = -INFINITY, L = 0.f;
@@ -875,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 20) tmem_dealloc(tmem, 512);
 }
 
 namespace {
