@@ -10,8 +10,8 @@
 //    converted once for both.
 //  * Work is cut by (row tile, key tile) as in kv8_decode.cu: CTA c of G owns an
 //    equal contiguous range of the list, whatever the lengths; a row tile's key
-//    tiles end with its last row's limit. Cut units go to the workspace and
-//    are joined in order by the CTA that finishes last.
+//    tiles end with its last row's limit. Parts of cut units go to the workspace,
+//    and a second kernel joins them in order.
 //  * Four warps read codes with 16-byte loads, a tile ahead, and write them as
 //    fp16 (exact) in the 128-byte-swizzled layout that tcgen05.mma reads; K and V
 //    have the same layout. q is fp16 times a power of two per row, which keeps
@@ -38,6 +38,7 @@ namespace {
 // Warps 0-15: softmax (slot = warp / 8, half of the keys = warp / 4 % 2), 16-19:
 // converters, 20 and 21: MMA (+ 2 idle).
 constexpr int kThreads = 768;
+constexpr int kJoinThreads = 256;
 constexpr int kRows = kKv8ChunkRows;
 constexpr int kRing = 8;       // tiles whose scales are kept: more than the stages ahead
 constexpr float kShift = 11.f; // P is held as 2^11 e^(s - m)
@@ -120,6 +121,39 @@ __device__ __forceinline__ void next_unit(const Kv8AttendParams& p, const int* p
     }
   }
   w.tiles = tiles_of(p, w.r, w.rt);
+}
+
+// prefix[b]: tiles before request b (by all of a block's threads); true to a lane
+// that met a bad request.
+__device__ __forceinline__ bool tiles_before(const Kv8AttendParams& p, int* prefix, int threads) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool any_bad = false;
+  for (int b = warp; b < p.B; b += threads / 32) {
+    bool bad;
+    const Request r = request_of(p, b, &bad);
+    any_bad |= bad;
+    int sum = 0;
+    for (int rt = lane; rt < r.row_tiles; rt += 32) sum += tiles_of(p, r, rt);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) prefix[b + 1] = sum * p.Hkv;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += up;
+      }
+      if (b0 + lane < p.B) prefix[b0 + lane + 1] = base + v;
+      base += __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (lane == 0) prefix[0] = 0;
+  }
+  return any_bad;
 }
 
 struct Scales {
@@ -306,46 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
   int* prefix = reinterpret_cast<int*>(sm + C::kOffPrefix);  // [B + 1] tiles before request b
-  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2], join;
+  __shared__ uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2];
   __shared__ uint64_t k_full[S], v_full[S], empty[S], sc_full[kRing], nan_full[kRing], lead[kRing];
   __shared__ __align__(16) Scales ring[kRing];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ int s_last;
   __shared__ float row_fs[2][128], row_l[2][2][128], row_m[2][2][2][128];  // what a row's two threads exchange
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- tiles before each request
   {
-    bool any_bad = false;
-    for (int b = warp; b < p.B; b += kThreads / 32) {
-      bool bad;
-      const Request r = request_of(p, b, &bad);
-      any_bad |= bad;
-      int sum = 0;
-      for (int rt = lane; rt < r.row_tiles; rt += 32) sum += tiles_of(p, r, rt);
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane == 0) prefix[b + 1] = sum * p.Hkv;
-    }
+    const bool any_bad = tiles_before(p, prefix, kThreads);
     if (any_bad && lane == 0 && blockIdx.x == 0) atomicOr(p.status, kDevBounds);
     if (tid == 0 && blockIdx.x == 0) p.status[1] = p.header_bytes;
-    __syncthreads();
-    if (warp == 0) {
-      int base = 0;
-      for (int b0 = 0; b0 < p.B; b0 += 32) {
-        int v = b0 + lane < p.B ? prefix[b0 + lane + 1] : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, v, d);
-          if (lane >= d) v += up;
-        }
-        if (b0 + lane < p.B) prefix[b0 + lane + 1] = base + v;
-        base += __shfl_sync(0xffffffffu, v, 31);
-      }
-      if (lane == 0) prefix[0] = 0;
-    }
     if (tid == 0) {
       for (int x = 0; x < 2; ++x) {
         mbar_init(&q_full[x], 4);  // (by warp)
@@ -364,7 +371,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         mbar_init(&nan_full[s], 4);
         mbar_init(&lead[s], 1);
       }
-      mbar_init(&join, 16);
       fence_barrier_init();
       abort_flag = 0;
     }
@@ -617,13 +623,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     const uint32_t tS = tmem + lanes + 128 * x + 64 * half, tO = tmem + lanes + 256 + 128 * x;
     const int pair = 1 + 4 * x + (warp & 3);
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
-    uint32_t cnt = 0, segs = 0, joins = 0;
+    uint32_t cnt = 0, segs = 0;
     bool ok = true;
-    // every softmax thread has got here (bounded)
-    auto softmax_sync = [&]() {
-      warp_arrive(&join);
-      ok &= warp_wait(&join, joins++ & 1, &abort_flag, p.status);
-    };
     // a row of q into the slot's tile, as fp16 times a power of two
     auto load_q = [&](const Walk& w) {
       if (half != 0 || (x == 1 && rows_of(p, w.r, w.rt) <= 128)) return;
@@ -833,52 +834,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
               make_float2(m == -INFINITY ? -INFINITY : rf, l);
         tc_fence_before();
       }
-      if (!whole) {
-        // ---- the last CTA of a cut unit joins its parts in order
-        const int first_tile = begin + n0 - seg - here.tile, last_tile = first_tile + here.tiles - 1;
-        const int c0 = static_cast<int>(((first_tile + 1ll) * G - 1) / total);
-        const int c1 = static_cast<int>(((last_tile + 1ll) * G - 1) / total);
-        softmax_sync();
-        if (tid == 0 && ok) {
-          __threadfence();
-          s_last = atomicInc(p.counters + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
-          __threadfence();
-        }
-        softmax_sync();
-        if (ok && s_last) {
-          const int begin0 = static_cast<int>(static_cast<long long>(c0) * total / G);
-          const size_t slot0 = 2 * static_cast<size_t>(c0) + (begin0 == first_tile ? 0 : 1);
-          for (int e = tid; e < rows * (D / 4); e += 512) {
-            const int r = e / (D / 4), d = 4 * (e % (D / 4));
-            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            float M = -INFINITY, L = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const size_t at = (c == c0 ? slot0 : 2 * static_cast<size_t>(c)) * kRows + r;
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + 2 * at));
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
-              const float mn = fmaxf(M, ml.x);
-              if (mn == -INFINITY) {
-                L += ml.y;
-                continue;
-              }
-              const float a = ex2_approx(M - mn), b = ex2_approx(ml.x - mn);
-              sum = make_float4(sum.x * a + y.x * b, sum.y * a + y.y * b, sum.z * a + y.z * b, sum.w * a + y.w * b);
-              L = L * a + ml.y * b;
-              M = mn;
-            }
-            const int rr = here.rt * kRows + r, head = here.kvh * p.g + rr % p.g;
-            const size_t token = here.r.q0 + rr / p.g;
-            const float inv = L != 0.f ? 1.f / L : 0.f;
-            uint2 y;
-            y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
-            y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
-            *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
-            if (d == 0 && p.lse)
-              p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-                  L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
-          }
-        }
-      }
     }
   }
 
@@ -886,6 +841,71 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == 20) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the units that CTAs cut, in order: block (c, y) rows 32 y ..
+// of the unit that CTA c began and did not finish. (One CTA joining a unit's parts
+// by itself took 50 us for 24 of them.)
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttendParams p) {
+  extern __shared__ int prefix[];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  tiles_before(p, prefix, kJoinThreads);
+  __syncthreads();
+  const int total = prefix[p.B], G = imin(static_cast<int>(gridDim.x), total);
+  const int c0 = blockIdx.x;
+  if (c0 >= G) return;
+  const int begin = static_cast<int>(static_cast<long long>(c0) * total / G);
+  const int end = static_cast<int>(static_cast<long long>(c0 + 1) * total / G);
+  const Walk w = walk_to(p, prefix, end - 1);
+  const int first_tile = end - 1 - w.tile;
+  const long long last_tile = static_cast<long long>(first_tile) + w.tiles - 1;
+  const int row0 = 32 * blockIdx.y, rows = imin(32, rows_of(p, w.r, w.rt) - row0);
+  if (first_tile < begin || last_tile < end || rows <= 0) return;
+  // CTA of list index x: the largest c with floor(c * total / G) <= x
+  const int c1 = static_cast<int>(((last_tile + 1) * G - 1) / total);
+  const int slot0 = begin == first_tile ? 0 : 1;
+  for (int e = threadIdx.x; e < rows * (D / 4); e += kJoinThreads) {
+    const int r = row0 + e / (D / 4), d = 4 * (e % (D / 4));
+    auto part = [&](int c) { return (2 * static_cast<size_t>(c) + (c == c0 ? slot0 : 0)) * kRows + r; };
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, L = 0.f;
+    for (int c = c0; c <= c1; c += 4) {  // (four parts' loads at a time)
+      float2 ml[4];
+      float4 y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.f);
+        y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + j <= c1) {
+          ml[j] = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(c + j));
+          y[j] = *reinterpret_cast<const float4*>(p.part_o + part(c + j) * D + d);
+        }
+      }
+      const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: sums of 0 (or NaN)
+      const float a = ex2_approx(M - ref);
+      sum = make_float4(sum.x * a, sum.y * a, sum.z * a, sum.w * a);
+      L = M == -INFINITY ? L : L * a;
+      M = mn;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float b = ex2_approx(ml[j].x - ref);
+        sum = make_float4(sum.x + y[j].x * b, sum.y + y[j].y * b, sum.z + y[j].z * b, sum.w + y[j].w * b);
+        L += ml[j].x == -INFINITY ? ml[j].y : ml[j].y * b;
+      }
+    }
+    const int rr = w.rt * kRows + r, head = w.kvh * p.g + rr % p.g;
+    const size_t token = w.r.q0 + rr / p.g;
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    uint2 y;
+    y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
+    y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
+    *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
+    if (d == 0 && p.lse)
+      p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
+          L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+  }
 }
 
 namespace {
@@ -896,8 +916,22 @@ cudaError_t launch(const Kv8AttendParams& p, int slot, int sms, cudaStream_t str
   const cudaError_t e = set_smem_attr_once((const void*)kv8_chunk_kernel<D, kType>, slot, dev,
                                            Cfg<D>::bytes(kMaxRequests));
   if (e != cudaSuccess) return e;
-  kv8_chunk_kernel<D, kType><<<imin(kKv8ChunkMaxCtas, sms), kThreads, Cfg<D>::bytes(p.B), stream>>>(p);
-  return cudaGetLastError();
+  const int grid = imin(kKv8ChunkMaxCtas, sms);
+  kv8_chunk_kernel<D, kType><<<grid, kThreads, Cfg<D>::bytes(p.B), stream>>>(p);
+  const cudaError_t launched = cudaGetLastError();
+  if (launched != cudaSuccess) return launched;
+  // the join's launch overlaps the end of the attention
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, kRows / 32);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = (p.B + 1) * sizeof(int);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, p);
 }
 }  // namespace
 

@@ -379,7 +379,8 @@ def _attend(q, cu, lens, table, kp, vp, ks, vs, max_new=None, max_kv=None, ws=No
     ([300], [129], 8, 2, 128, 64, E4M3), ([900, 77], [100, 40], 16, 2, 64, 128, INT8),
     ([20000, 5, 1300], [300, 5, 17], 16, 2, 128, 64, E4M3), ([700] * 5, [33] * 5, 8, 1, 64, 16, INT8),
     ([4097], [257], 8, 1, 128, 16, E4M3), ([130, 131], [130, 1], 1, 1, 128, 32, INT8),
-    ([9000], [20], 7, 1, 64, 32, E4M3), ([600, 0, 2000], [600, 0, 555], 16, 8, 128, 128, INT8),
+    ([9000], [20], 7, 1, 64, 32, E4M3), ([40000], [16], 8, 1, 128, 64, E4M3), ([60000], [34], 8, 1, 64, 64, INT8),
+    ([129, 30000, 700, 5000], [18, 16, 20, 33], 8, 1, 128, 16, E4M3), ([600, 0, 2000], [600, 0, 555], 16, 8, 128, 128, INT8),
     # requests without tokens or keys, rows that see nothing
     ([10, 0, 20, 0], [1, 0, 0, 1], 4, 1, 64, 16, E4M3), ([3], [7], 4, 2, 64, 16, E4M3),
     ([0, 0], [2, 1], 8, 1, 128, 32, INT8), ([0], [40], 4, 1, 64, 16, E4M3)])
@@ -476,9 +477,10 @@ def test_attend_bad_pages_and_lengths():
     assert _status(ws) == BOUNDS and bool((o[2] == 3.0).all())
 
 
-def test_attend_strides_padding_and_repeats():
+@pytest.mark.parametrize("new", [[2, 1, 2], [40, 3, 70]])
+def test_attend_strides_padding_and_repeats(new):
     """q as heads of a fused buffer, padded rows untouched, and the same bits every time."""
-    lens, new = [513, 40, 2000], [2, 1, 2]
+    lens = [513, 40, 2000]
     q, cu, *rest = _attend_case(lens, new, 8, 2, 128, 64, E4M3, 29, pad=3)
     n = q.shape[0]
     fused = torch.zeros(n, 12, 128, dtype=torch.bfloat16, device="cuda")
@@ -512,6 +514,83 @@ def test_attend_on_two_streams_with_two_workspaces():
     for os_ in outs:
         for o in os_:
             assert torch.equal(o, want)
+
+
+def test_attend_one_workspace_for_calls_of_many_shapes():
+    """Calls of other batches, row counts and kernels leave a workspace as they found it."""
+    shapes = [([5000], [1], 8, 2, 64, 16, E4M3), ([900, 77, 3000], [100, 40, 20], 16, 2, 64, 128, INT8),
+              ([300] * 9, [2] * 9, 32, 8, 128, 32, E4M3), ([20000], [60], 8, 1, 128, 64, E4M3),
+              ([9, 4000], [7, 4], 4, 1, 64, 16, INT8), ([70001], [1], 8, 2, 128, 64, E4M3)]
+    ws = star.alloc_workspace(star.star_kv8_attend_workspace_bytes(9, 200, 32, 8, 128, 100))
+    for seed, (lens, new, *rest) in enumerate(shapes + shapes[::-1]):
+        case = _attend_case(lens, new, *rest, 40 + seed)
+        a = _attend(case[0], case[1], lens, *case[2:], ws=ws)[:2]
+        b = _attend(case[0], case[1], lens, *case[2:])[:2]
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert _status(ws) == "STAR_OK"
+
+
+def test_attend_many_requests():
+    rng = random.Random(3)
+    lens = [rng.choice([0, 1, 5, 16, 17, 100, 300]) for _ in range(4096)]
+    new = [min(n, 1) for n in lens]
+    case = _attend_case(lens, new, 2, 1, 64, 16, E4M3, 51)
+    o, lse, ws = _attend(case[0], case[1], lens, *case[2:])
+    U.check_attend(o, lse, U.attend_plain(case[0], case[1], lens, *case[2:]))
+    assert _status(ws) == "STAR_OK"
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_pools_beyond_32_bit_offsets(new):
+    """Pages whose bytes lie more than 2^32 into the pool, for the append and both attention kernels."""
+    page, h, d, kind, pages = 128, 8, 128, INT8, 36000  # 4.7 GB each for K and V
+    kp = torch.empty(pages, h, page, d, dtype=kind, device="cuda")
+    vp = torch.empty_like(kp)
+    ks, vs = torch.zeros(pages, h, device="cuda"), torch.zeros(pages, h, device="cuda")
+    ids = [pages - 1, 3, pages - 2]
+    n = 300
+    k, v = _kv(n, h, d, 61)
+    slots = [ids[t // page] * page + t % page for t in range(n)]
+    ws = star.alloc_workspace(256)
+    star.star_kv8_append(k, v, ints(slots), ints([0, page, 2 * page, n]), kp, vp, ks, vs, ws)
+    assert _status(ws) == "STAR_OK"
+    sub = torch.tensor(ids, device="cuda")
+    wk, wv = U.Pages(torch.zeros(3, h, page, d, dtype=kind)), U.Pages(torch.zeros(3, h, page, d, dtype=kind))
+    sk, sv = torch.zeros(3, h, dtype=torch.float64), torch.zeros(3, h, dtype=torch.float64)
+    runs, local = [0, page, 2 * page, n], list(range(n))
+    U.append_plain(k.double().cpu(), runs, local, wk, sk, page)
+    U.append_plain(v.double().cpu(), runs, local, wv, sv, page)
+    rows = torch.arange(3 * page).view(3, 1, page, 1) < n
+    for got, want in ((kp, wk), (vp, wv)):
+        assert torch.equal(torch.where(rows, got[sub].double().cpu(), 0.0), torch.where(rows, want.values, 0.0))
+    assert torch.equal(ks[sub].double().cpu(), sk) and torch.equal(vs[sub].double().cpu(), sv)
+    q = torch.randn(new, 2 * h, d, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
+    o, lse, _ = _attend(q, [0, new], [n], ints([ids]), kp, vp, ks, vs)
+    small = [t[sub].contiguous() for t in (kp, vp, ks, vs)]
+    U.check_attend(o, lse, U.attend_plain(q, [0, new], [n], ints([[0, 1, 2]]), *small))
+
+
+def test_attend_chunk_captured_and_replayed():
+    """A captured call of many new tokens follows lengths that change between replays."""
+    case = _attend_case([3000, 2000], [60, 40], 8, 2, 128, 64, E4M3, 71)
+    q, cu, table, kp, vp, ks, vs = case
+    cu_t, kv_t = ints(cu), ints([3000, 2000])
+    o, lse = torch.zeros_like(q), torch.zeros(8, 100, device="cuda")
+    ws = star.alloc_workspace(star.star_kv8_attend_workspace_bytes(2, 100, 8, 2, 128, 100))
+    call = lambda: star.star_kv8_attend(q, cu_t, kv_t, table, kp, vp, ks, vs, o, ws, 100, 3000, lse=lse)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for c, lens in (([0, 60, 100], [3000, 2000]), ([0, 100, 100], [2900, 0]), ([0, 1, 100], [1, 1999])):
+        cu_t.copy_(ints(c))
+        kv_t.copy_(ints(lens))
+        for t in (kp, vp):  # NaN behind the last key must not matter: these lengths end elsewhere
+            t.view(torch.uint8)[(t.view(torch.uint8) & 0x7F) == 0x7F] = 0
+        graph.replay()
+        U.check_attend(o, lse, U.attend_plain(q, c, lens, table, kp, vp, ks, vs))
+    assert _status(ws) == "STAR_OK"
 
 
 # ---- together -----------------------------------------------------------------------------------------
