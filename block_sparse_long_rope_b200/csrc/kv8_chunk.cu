@@ -345,9 +345,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   __shared__ __align__(16) Scales ring[kRing];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ float row_fs[2][128], row_l[2][2][128], row_m[2][2][2][128];  // what a row's two threads exchange
+  // what a row's two threads exchange
+  __shared__ float row_l[2][2][128], row_m[2][2][2][128];
+  __shared__ uint32_t row_q[2][2][128];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the join may be launched where there is room: it waits for this kernel's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   {
     const bool any_bad = tiles_before(p, prefix, kThreads);
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     if (tid == 0 && blockIdx.x == 0) p.status[1] = p.header_bytes;
     if (tid == 0) {
       for (int x = 0; x < 2; ++x) {
-        mbar_init(&q_full[x], 4);  // (by warp)
+        mbar_init(&q_full[x], 8);  // (by warp)
         mbar_init(&s_full[x], 1);
         mbar_init(&p_full[x], 8);
         mbar_init(&o_full[x], 1);
@@ -625,34 +629,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory"); };
     uint32_t cnt = 0, segs = 0;
     bool ok = true;
-    // a row of q into the slot's tile, as fp16 times a power of two
+    float next_fs = 0.f;
+    // a row of q into the slot's tile, as fp16 times a power of two: half of it by
+    // each of its threads
     auto load_q = [&](const Walk& w) {
-      if (half != 0 || (x == 1 && rows_of(p, w.r, w.rt) <= 128)) return;
+      if (x == 1 && rows_of(p, w.r, w.rt) <= 128) return;
       const int r = w.rt * kRows + 128 * x + row;
-      const bool real = r < w.r.T * p.g;
       uint8_t* dst = sm + x * C::kTile;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          p.q + (w.r.q0 + (real ? r / p.g : 0)) * p.qs[0] + (w.kvh * p.g + (real ? r % p.g : 0)) * p.qs[1]);
+      uint4 v[D / 16];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < w.r.T * p.g) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (w.r.q0 + r / p.g) * p.qs[0] +
+                                                          (w.kvh * p.g + r % p.g) * p.qs[1]) + half * (D / 16);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) v[i] = __ldg(src + i);
+      }
       uint32_t top = 0;
-      if (real)
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = __ldg(src + i);
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                                       __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-        }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+      row_q[x][half][row] = top;
+      pair_sync();
+      top = __vmaxu2(top, row_q[x][half ^ 1][row]);
       const int e = static_cast<int>(imax(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent
       const int up = imin(254, imax(1, 127 + 14 - (e - 127)));  // 2^(14 - (e - 127)), a normal number
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
       // this row's factor: 2^-e log2(e) / sqrt(D)
-      row_fs[x][row] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
+      next_fs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
       auto two = [&](uint32_t u) { return half2_of(bf16_lo(u) * mul, bf16_hi(u) * mul); };
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (real) v = __ldg(src + i);
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        const int i = half * (D / 16) + j;
         *reinterpret_cast<uint4*>(dst + (i >> 3) * C::kHalf + sw128_offset(row, i & 7)) =
-            make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
+            make_uint4(two(v[j].x), two(v[j].y), two(v[j].z), two(v[j].w));
       }
       fence_async_shared();
       warp_arrive(&q_full[x]);
@@ -670,12 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // keys that the slot's and the unit's first rows see
       const int lim_lo = keys_of_row(p, here.r, here.rt * kRows + 128 * x);
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
-      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f, fs = 0.f;
+      float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f, fs = next_fs;
       bool nan = false;
-      if (active) {
-        pair_sync();
-        fs = row_fs[x][row];
-      }
       for (int i = 0; i < seg; ++i) {
         const int n = n0 + i;
         const Scales& ss = ring[n % kRing];
@@ -849,19 +856,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttendParams p) {
   extern __shared__ int prefix[];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  // (the lengths were there before the attention began)
   tiles_before(p, prefix, kJoinThreads);
   __syncthreads();
   const int total = prefix[p.B], G = imin(static_cast<int>(gridDim.x), total);
-  const int c0 = blockIdx.x;
-  if (c0 >= G) return;
-  const int begin = static_cast<int>(static_cast<long long>(c0) * total / G);
-  const int end = static_cast<int>(static_cast<long long>(c0 + 1) * total / G);
-  const Walk w = walk_to(p, prefix, end - 1);
-  const int first_tile = end - 1 - w.tile;
-  const long long last_tile = static_cast<long long>(first_tile) + w.tiles - 1;
-  const int row0 = 32 * blockIdx.y, rows = imin(32, rows_of(p, w.r, w.rt) - row0);
-  if (first_tile < begin || last_tile < end || rows <= 0) return;
+  const int c0 = blockIdx.x, row0 = 32 * blockIdx.y;
+  Walk w{};
+  int begin = 0, first_tile = 0, rows = 0;
+  long long last_tile = 0;
+  if (c0 < G) {
+    begin = static_cast<int>(static_cast<long long>(c0) * total / G);
+    const int end = static_cast<int>(static_cast<long long>(c0 + 1) * total / G);
+    w = walk_to(p, prefix, end - 1);
+    first_tile = end - 1 - w.tile;
+    last_tile = static_cast<long long>(first_tile) + w.tiles - 1;
+    if (first_tile >= begin && last_tile >= end) rows = imin(32, rows_of(p, w.r, w.rt) - row0);
+  }
+  // the parts are there; every block waits, so that what follows this kernel
+  // also follows the attention
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (rows <= 0) return;
   // CTA of list index x: the largest c with floor(c * total / G) <= x
   const int c1 = static_cast<int>(((last_tile + 1) * G - 1) / total);
   const int slot0 = begin == first_tile ? 0 : 1;
