@@ -826,10 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
               dst[v] = y;
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + (part * kRows + 128 * x + row) * D + 32 * q);
+            // (a part is [D / 4][rows][4]: a warp's rows are neighbours)
+            float4* dst = reinterpret_cast<float4*>(p.part_o + part * kRows * D) + 8 * q * kRows + 128 * x + row;
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              dst[v] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
+              dst[v * kRows] = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
                                    __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
           }
         }
@@ -879,46 +880,66 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   // CTA of list index x: the largest c with floor(c * total / G) <= x
   const int c1 = static_cast<int>(((last_tile + 1) * G - 1) / total);
   const int slot0 = begin == first_tile ? 0 : 1;
-  for (int e = threadIdx.x; e < rows * (D / 4); e += kJoinThreads) {
-    const int r = row0 + e / (D / 4), d = 4 * (e % (D / 4));
-    auto part = [&](int c) { return (2 * static_cast<size_t>(c) + (c == c0 ? slot0 : 0)) * kRows + r; };
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, L = 0.f;
-    for (int c = c0; c <= c1; c += 4) {  // (four parts' loads at a time)
-      float2 ml[4];
-      float4 y[4];
+  // a thread takes four rows' elements d .. d + 3, two parts' loads at a time
+  constexpr int kVecs = D / 4;
+  static_assert(kJoinThreads * 4 == 32 * 32, "32 rows of D 128");
+  const int r0 = row0 + threadIdx.x % 8, v = threadIdx.x / 8;
+  if (v >= kVecs) return;
+  float4 sum[4];
+  float M[4], L[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        ml[j] = make_float2(-INFINITY, 0.f);
-        y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c + j <= c1) {
-          ml[j] = *reinterpret_cast<const float2*>(p.part_ml + 2 * part(c + j));
-          y[j] = *reinterpret_cast<const float4*>(p.part_o + part(c + j) * D + d);
+  for (int i = 0; i < 4; ++i) {
+    sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    M[i] = -INFINITY;
+    L[i] = 0.f;
+  }
+  for (int c = c0; c <= c1; c += 2) {
+    float2 ml[2][4];
+    float4 y[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 8 * i;
+        ml[j][i] = make_float2(-INFINITY, 0.f);
+        y[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + j <= c1 && r - row0 < rows) {
+          const size_t part = 2 * static_cast<size_t>(c + j) + (c + j == c0 ? slot0 : 0);
+          ml[j][i] = *reinterpret_cast<const float2*>(p.part_ml + 2 * (part * kRows + r));
+          y[j][i] = reinterpret_cast<const float4*>(p.part_o + part * kRows * D)[v * kRows + r];
         }
       }
-      const float mn = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
-      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: sums of 0 (or NaN)
-      const float a = ex2_approx(M - ref);
-      sum = make_float4(sum.x * a, sum.y * a, sum.z * a, sum.w * a);
-      L = M == -INFINITY ? L : L * a;
-      M = mn;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float b = ex2_approx(ml[j].x - ref);
-        sum = make_float4(sum.x + y[j].x * b, sum.y + y[j].y * b, sum.z + y[j].z * b, sum.w + y[j].w * b);
-        L += ml[j].x == -INFINITY ? ml[j].y : ml[j].y * b;
+    for (int i = 0; i < 4; ++i) {
+      const float mn = fmaxf(M[i], fmaxf(ml[0][i].x, ml[1][i].x));
+      const float ref = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: sums of 0 (or NaN)
+      const float a = ex2_approx(M[i] - ref);
+      sum[i] = make_float4(sum[i].x * a, sum[i].y * a, sum[i].z * a, sum[i].w * a);
+      L[i] = M[i] == -INFINITY ? L[i] : L[i] * a;
+      M[i] = mn;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float b = ex2_approx(ml[j][i].x - ref);
+        sum[i] = make_float4(sum[i].x + y[j][i].x * b, sum[i].y + y[j][i].y * b, sum[i].z + y[j][i].z * b,
+                             sum[i].w + y[j][i].w * b);
+        L[i] += ml[j][i].x == -INFINITY ? ml[j][i].y : ml[j][i].y * b;
       }
     }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 8 * i;
+    if (r - row0 >= rows) break;
     const int rr = w.rt * kRows + r, head = w.kvh * p.g + rr % p.g;
     const size_t token = w.r.q0 + rr / p.g;
-    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const float inv = L[i] != 0.f ? 1.f / L[i] : 0.f;
     uint2 y;
-    y.x = pack_bf16x2(sum.x * inv, sum.y * inv);
-    y.y = pack_bf16x2(sum.z * inv, sum.w * inv);
-    *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
-    if (d == 0 && p.lse)
+    y.x = pack_bf16x2(sum[i].x * inv, sum[i].y * inv);
+    y.y = pack_bf16x2(sum[i].z * inv, sum[i].w * inv);
+    *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + 4 * v) = y;
+    if (v == 0 && p.lse)
       p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-          L != 0.f ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+          L[i] != 0.f ? (M[i] + log2f(L[i])) * 0.6931471805599453f : -INFINITY;
   }
 }
 

@@ -64,7 +64,7 @@ struct Kv8AttendParams {
   int header_bytes;     // workspace bytes holding the status block and the counters
   unsigned* counters;   // [kKv8MaxCtas] finished parts of the unit that is cut at a CTA's end
   float* part_ml;       // [CTAs][2][rows][2] maximum (log2 units) and sum of a part
-  float* part_o;        // [CTAs][2][rows][D]
+  float* part_o;        // [CTAs][2][rows][D] ([D / 4][rows][4] of the chunk kernel)
 };
 constexpr int kKv8Tile = 128;     // keys of one tile of a CTA
 constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many (decode)
