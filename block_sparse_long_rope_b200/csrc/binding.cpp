@@ -126,6 +126,11 @@ Cache cache(const at::Tensor& kp, const at::Tensor& vp, const at::Tensor& ks, co
   c.dim = as_int(kp.size(3), "D");
   return c;
 }
+const at::Tensor& space(PyObject* o) {
+  const at::Tensor& t = tensor(o, "workspace");
+  if (!t.is_contiguous()) raise(PyExc_ValueError, "workspace must be contiguous");
+  return t;
+}
 size_t bytes(const at::Tensor& t) { return static_cast<size_t>(t.numel()) * t.element_size(); }
 
 // Runs one entry point's body with n arguments; nothing but a Python error leaves it.
@@ -211,7 +216,7 @@ PyObject* batch_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &ctx = ints(a[0], "ctx_len", B), &add = ints(a[1], "new_len", B), &kv = ints(a[10], "kv_len", B),
                      &cu = ints(a[6], "cu_new", B + 1), &slot = ints(a[8], "slot", cap),
                      &begin = ints(a[3], "free_begin", 1), &next = ints(a[11], "free_next", 1),
-                     &runs = ints(a[9], "run_start"), &ws = tensor(a[12], "workspace");
+                     &runs = ints(a[9], "run_start"), &ws = space(a[12]);
     Place place;
     place.on(table, "block_table");
     place.on(ctx, "ctx_len");
@@ -251,7 +256,7 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (t.stride(2) != 1) raise(PyExc_ValueError, "%s must be contiguous in head_dim", names[i]);
     }
     const at::Tensor &slot = ints(a[2], "slot", k.size(0)), &runs = ints(a[3], "run_start"),
-                     &ws = tensor(a[8], "workspace");
+                     &ws = space(a[8]);
     Place place;
     place.on(k, "k");
     place.on(v, "v");
@@ -285,7 +290,7 @@ PyObject* kv8_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& table = ints(a[3], "block_table");
     if (table.dim() != 2) raise(PyExc_ValueError, "block_table must be [B, max_pages]");
     const at::Tensor &cu = ints(a[1], "cu_new", table.size(0) + 1), &kv = ints(a[2], "kv_len", table.size(0)),
-                     &ws = tensor(a[9], "workspace");
+                     &ws = space(a[9]);
     Place place;
     place.on(q, "q");
     place.on(o, "o");

@@ -381,6 +381,8 @@ def _attend(q, cu, lens, table, kp, vp, ks, vs, max_new=None, max_kv=None, ws=No
     ([4097], [257], 8, 1, 128, 16, E4M3), ([130, 131], [130, 1], 1, 1, 128, 32, INT8),
     ([9000], [20], 7, 1, 64, 32, E4M3), ([40000], [16], 8, 1, 128, 64, E4M3), ([60000], [34], 8, 1, 64, 64, INT8),
     ([129, 30000, 700, 5000], [18, 16, 20, 33], 8, 1, 128, 16, E4M3), ([600, 0, 2000], [600, 0, 555], 16, 8, 128, 128, INT8),
+    # many query heads on one KV head
+    ([1000, 40], [1, 1], 64, 1, 128, 64, E4M3), ([500], [1], 24, 1, 64, 16, INT8), ([300], [2], 96, 2, 128, 32, E4M3),
     # requests without tokens or keys, rows that see nothing
     ([10, 0, 20, 0], [1, 0, 0, 1], 4, 1, 64, 16, E4M3), ([3], [7], 4, 2, 64, 16, E4M3),
     ([0, 0], [2, 1], 8, 1, 128, 32, INT8), ([0], [40], 4, 1, 64, 16, E4M3)])
@@ -457,6 +459,27 @@ def test_attend_later_nan_does_not_reach_earlier_tokens(new):
     assert torch.isnan(o[new - 2:, :, 9]).all() and torch.isfinite(lse).all()
 
 
+def test_attend_missing_pages_of_a_chunk():
+    """Keys of pages that do not exist are invisible, a whole first tile of them too."""
+    lens, new = [600, 300], [50, 40]
+    q, cu, table, kp, vp, ks, vs = _attend_case(lens, new, 4, 1, 64, 16, E4M3, 24)
+    table[0, 3], table[0, 36], table[1, 5] = -1, kp.shape[0], 2 ** 31 - 1
+    table[1, :8] = -7
+    o, lse, ws = _attend(q, cu, lens, table, kp, vp, ks, vs)
+    U.check_attend(o, lse, U.attend_plain(q, cu, lens, table, kp, vp, ks, vs))
+    assert _status(ws) == BOUNDS and _status(ws) == "STAR_OK"
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_attend_without_lse(new):
+    lens = [700, 90]
+    q, cu, *rest = _attend_case(lens, [new, new], 8, 2, 64, 32, INT8, 25)
+    want, _, ws = _attend(q, cu, lens, *rest)
+    o = torch.empty_like(want)
+    star.star_kv8_attend(q, ints(cu), ints(lens), *rest, o, ws, new, 700)
+    assert torch.equal(o, want)
+
+
 def test_attend_bad_pages_and_lengths():
     lens, new = [100, 100, 100], [1, 1, 1]
     q, cu, table, kp, vp, ks, vs = _attend_case(lens, new, 4, 1, 64, 16, INT8, 23)
@@ -495,9 +518,10 @@ def test_attend_strides_padding_and_repeats(new):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-def test_attend_on_two_streams_with_two_workspaces():
+@pytest.mark.parametrize("new", [1, 70])
+def test_attend_on_two_streams_with_two_workspaces(new):
     lens = [20000]
-    q, cu, *rest = _attend_case(lens, [1], 8, 2, 64, 64, E4M3, 31)
+    q, cu, *rest = _attend_case(lens, [new], 8, 2, 64, 64, E4M3, 31)
     want, _, _ = _attend(q, cu, lens, *rest)
     cu_t, kv_t = ints(cu), ints(lens)
     torch.cuda.synchronize()
@@ -505,11 +529,11 @@ def test_attend_on_two_streams_with_two_workspaces():
     outs, spaces = [], []
     for s in streams:
         outs.append([torch.empty_like(want) for _ in range(8)])
-        spaces.append(star.alloc_workspace(star.star_kv8_attend_workspace_bytes(1, 1, 8, 2, 64, 1)))
+        spaces.append(star.alloc_workspace(star.star_kv8_attend_workspace_bytes(1, new, 8, 2, 64, new)))
     torch.cuda.synchronize()
     for i in range(8):
         for s, o, ws in zip(streams, outs, spaces):
-            star.star_kv8_attend(q, cu_t, kv_t, *rest, o[i], ws, 1, 20000, stream=s)
+            star.star_kv8_attend(q, cu_t, kv_t, *rest, o[i], ws, new, 20000, stream=s)
     torch.cuda.synchronize()
     for os_ in outs:
         for o in os_:

@@ -260,6 +260,7 @@ def _cpu_attend():
     (dict(kv_len=torch.zeros(1, dtype=torch.int64)), ValueError),
     (dict(block_table=torch.zeros(4, dtype=torch.int32)), ValueError),
     (dict(lse=torch.zeros(4, 2)), ValueError),
+    (dict(workspace=torch.zeros(256, 2, dtype=torch.uint8)[:, 0]), ValueError),
     (dict(o=torch.zeros(4, 1, 64, dtype=torch.bfloat16).transpose(0, 1)), ValueError)])
 def test_attend_binding_refusals(change, error):
     args = _cpu_attend()
