@@ -64,19 +64,19 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
   const int first = !pairs ? 16 * u : kInter ? 16 * u : 8 * u;    // this unit's two vectors
   const int second = !pairs || kInter ? first + 8 : first + half;
   const bool mine = t < ntok && (pairs || p.copy_rest);
-  const __nv_bfloat16* x = p.x + b * p.xs[0] + (tok0 + static_cast<long long>(t)) * p.xs[1];
-  __nv_bfloat16* y = p.y + b * p.ys[0] + (tok0 + static_cast<long long>(t)) * p.ys[1];
+  const __nv_bfloat16* x = p.x + b * p.xs[0] + (tok0 + static_cast<long long>(t)) * p.xs[1] + h * p.xs[2] + first;
+  __nv_bfloat16* y = p.y + b * p.ys[0] + (tok0 + static_cast<long long>(t)) * p.ys[1] + h * p.ys[2] + first;
+  const long long x_step = per * p.xs[2], y_step = per * p.ys[2];  // to this thread's next head
+  const int gap = second - first;
 
   uint4 lo[kBatch], hi[kBatch];
   auto load = [&]() {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int hh = h + i * per;
-      if (mine && hh < h_end) {
-        lo[i] = *reinterpret_cast<const uint4*>(x + hh * p.xs[2] + first);
-        hi[i] = *reinterpret_cast<const uint4*>(x + hh * p.xs[2] + second);
+    for (int i = 0; i < kBatch; ++i, x += x_step)
+      if (mine && h + i * per < h_end) {
+        lo[i] = *reinterpret_cast<const uint4*>(x);
+        hi[i] = *reinterpret_cast<const uint4*>(x + gap);
       }
-    }
   };
   load();
   for (int e = threadIdx.x; e < ntok * half; e += kThreads) {
@@ -104,9 +104,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
   // Units of a row's copied part and its pairs sit in different lanes of a warp
   while (h < h_end) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int hh = h + i * per;
-      if (hh >= h_end) break;
+    for (int i = 0; i < kBatch; ++i, y += y_step) {
+      if (h + i * per >= h_end) break;
       uint32_t* l = reinterpret_cast<uint32_t*>(&lo[i]);
       uint32_t* r = reinterpret_cast<uint32_t*>(&hi[i]);
       if (pairs) {
@@ -152,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
           }
         }
       }
-      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + first) = lo[i];
-      *reinterpret_cast<uint4*>(y + hh * p.ys[2] + second) = hi[i];
+      *reinterpret_cast<uint4*>(y) = lo[i];
+      *reinterpret_cast<uint4*>(y + gap) = hi[i];
     }
     h += kBatch * per;
     load();
