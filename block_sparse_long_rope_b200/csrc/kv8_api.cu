@@ -99,9 +99,9 @@ struct AttendLayout {
   size_t part_ml, part_o, total;
 };
 constexpr size_t kAttendHeader = star::kStatusBytes + star::kKv8MaxCtas * sizeof(unsigned);
-AttendLayout attend_layout(int Hq, int Hkv, int D, int max_new) {
+AttendLayout attend_layout(int rows, int D) {
   AttendLayout l;
-  l.rows = star::kv8_rows(max_new, Hq / Hkv);
+  l.rows = rows;
   const size_t ctas = l.rows == star::kKv8ChunkRows ? star::kKv8ChunkMaxCtas : star::kKv8MaxCtas;
   const size_t parts = 2 * ctas * l.rows;
   l.part_ml = kAttendHeader;
@@ -318,7 +318,7 @@ star_status star_kv8_append(const void* k, const int64_t k_stride[2], const void
 size_t star_kv8_attend_workspace_bytes(int B, int n_tokens, int Hq, int Hkv, int D, int max_new) {
   (void)n_tokens;
   if (B < 1 || Hq < 1 || Hkv < 1 || D < 1 || max_new < 1 || Hq % Hkv) return star::kStatusBytes;
-  return attend_layout(Hq, Hkv, D, max_new).total;
+  return attend_layout(star::kv8_rows(max_new, Hq / Hkv), D).total;
 }
 
 star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_tokens,
@@ -352,13 +352,19 @@ star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_toke
   // what the kernels count in 32 bits: rows of a request, tiles of a call
   if ((long long)max_new * g > (1 << 24))
     return fail(STAR_ERR_INVALID_ARG, "max_new * Hq / Hkv (%lld) must be at most 2^24", (long long)max_new * g);
-  const AttendLayout lay = attend_layout(Hq, Hkv, D, max_new);
-  const int row_tiles = (max_new * g + lay.rows - 1) / lay.rows;
-  const double tiles = (double)B * Hkv * row_tiles * ((max_kv - 1) / star::kKv8Tile + 1);
+  // tiles of a call with row tiles of this many rows
+  auto tiles_with = [&](int rows) {
+    return (double)B * Hkv * ((max_new * g + rows - 1) / rows) * ((max_kv - 1) / star::kKv8Tile + 1);
+  };
+  const size_t need = attend_layout(star::kv8_rows(max_new, g), D).total;
+  const int rows = star::kv8_rows(max_new, g) == star::kKv8ChunkRows && tiles_with(16) <= star::kKv8FewTiles
+                       ? 16 : star::kv8_rows(max_new, g);
+  const AttendLayout lay = attend_layout(rows, D);
+  const double tiles = tiles_with(rows);
   if (tiles > 2147483647.0)
     return fail(STAR_ERR_INVALID_ARG, "problem too large: %.0f tiles of %d rows by %d keys", tiles,
                 lay.rows, star::kKv8Tile);
-  if ((s = check_workspace(workspace, workspace_bytes, lay.total))) return s;
+  if ((s = check_workspace(workspace, workspace_bytes, need))) return s;
   const int sms = star::device_sms();
   if (sms <= 0) return STAR_ERR_UNSUPPORTED;
   if (n_tokens == 0) return ok();

@@ -78,6 +78,12 @@ inline int kv8_rows(int max_new, int g) {
   const long long rows = (long long)max_new * g;
   return rows <= 8 ? 8 : rows <= 32 ? 16 : kKv8ChunkRows;
 }
+// A call of more rows stays on the decode kernel while it has at most this many
+// tiles of 16 rows by 128 keys, since the chunk kernel needs 15 us before its first
+// product: 240 rows on 3000 keys of D 64 (360 tiles) 15.5 us against 25, 200 rows of
+// 8 heads on 1000 keys (832) 21.7 against 25; 40 rows of 16 requests, 8 heads on 500
+// keys (1536) 37 against 31, 1024 rows of 8 heads on 600 keys (2560) 48 against 34.
+constexpr int kKv8FewTiles = 1024;
 cudaError_t launch_kv8_decode(const Kv8AttendParams& p, int D, int kv_type, int rows, int sms,
                               cudaStream_t stream);
 cudaError_t launch_kv8_chunk(const Kv8AttendParams& p, int D, int kv_type, int sms, cudaStream_t stream);

@@ -366,6 +366,14 @@ def _attend(q, cu, lens, table, kp, vp, ks, vs, max_new=None, max_kv=None, ws=No
     return o, lse, ws
 
 
+def _wide(table, page):
+    """(table, max_kv) of a call that may see 200,000 keys: more than 32 rows of a KV head then take the
+    kernel of many rows whatever the lengths are."""
+    pad = torch.full((table.shape[0], -(-200000 // page)), 2 ** 30, dtype=torch.int32, device="cuda")
+    pad[:, :table.shape[1]] = table
+    return pad, 200000
+
+
 @pytest.mark.parametrize("lens,new,Hq,Hkv,D,page,kind", [
     ([1], [1], 1, 1, 64, 16, E4M3), ([1], [1], 4, 1, 64, 16, INT8), ([15], [1], 8, 1, 128, 16, E4M3),
     ([16], [1], 4, 2, 128, 32, INT8), ([17], [1], 32, 8, 128, 64, E4M3),
@@ -390,8 +398,14 @@ def test_attend(lens, new, Hq, Hkv, D, page, kind):
     case = _attend_case(lens, new, Hq, Hkv, D, page, kind, 7)
     q, cu, table = case[:3]
     o, lse, ws = _attend(q, cu, lens, *case[2:])
-    U.check_attend(o, lse, U.attend_plain(q, cu, lens, *case[2:]))
+    want = U.attend_plain(q, cu, lens, *case[2:])
+    U.check_attend(o, lse, want)
     assert _status(ws) == "STAR_OK"
+    if max(new) * Hq // Hkv > 32:
+        table, max_kv = _wide(table, page)
+        o, lse, ws = _attend(q, cu, lens, table, *case[3:], max_kv=max_kv)
+        U.check_attend(o, lse, want)
+        assert _status(ws) == "STAR_OK"
 
 
 @pytest.mark.parametrize("kind", [E4M3, INT8])
@@ -400,8 +414,10 @@ def test_attend_peaked_scores_and_uneven_scales(kind, new):
     """Large queries (one key takes all) and page scales that differ by powers up to 2^20."""
     lens = [777, 2100]
     case = _attend_case(lens, [new, new], 8, 2, 128, 32, kind, 11, q_scale=12.0, spread=5.0)
-    o, lse, _ = _attend(case[0], case[1], lens, *case[2:])
-    U.check_attend(o, lse, U.attend_plain(case[0], case[1], lens, *case[2:]))
+    want = U.attend_plain(case[0], case[1], lens, *case[2:])
+    for table, max_kv in ((case[2], 2100), _wide(case[2], 32)):
+        o, lse, _ = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)
+        U.check_attend(o, lse, want)
 
 
 def test_attend_flat_tail_behind_a_peak():
@@ -453,10 +469,11 @@ def test_attend_later_nan_does_not_reach_earlier_tokens(new):
     vp.view(torch.uint8)[int(table[0, bad // 16]), 0, bad % 16, 9] = 0xFF
     clean = vp.clone()
     clean.view(torch.uint8)[int(table[0, bad // 16]), 0, bad % 16, 9] = 0
-    o, lse, _ = _attend(q, cu, [L], table, kp, vp, ks, vs)
-    ref, _, _ = _attend(q, cu, [L], table, kp, clean, ks, vs)
-    assert torch.equal(o[:new - 2], ref[:new - 2])
-    assert torch.isnan(o[new - 2:, :, 9]).all() and torch.isfinite(lse).all()
+    for tab, max_kv in ((table, L), _wide(table, 16)):
+        o, lse, _ = _attend(q, cu, [L], tab, kp, vp, ks, vs, max_kv=max_kv)
+        ref, _, _ = _attend(q, cu, [L], tab, kp, clean, ks, vs, max_kv=max_kv)
+        assert torch.equal(o[:new - 2], ref[:new - 2])
+        assert torch.isnan(o[new - 2:, :, 9]).all() and torch.isfinite(lse).all()
 
 
 def test_attend_missing_pages_of_a_chunk():
@@ -465,18 +482,21 @@ def test_attend_missing_pages_of_a_chunk():
     q, cu, table, kp, vp, ks, vs = _attend_case(lens, new, 4, 1, 64, 16, E4M3, 24)
     table[0, 3], table[0, 36], table[1, 5] = -1, kp.shape[0], 2 ** 31 - 1
     table[1, :8] = -7
-    o, lse, ws = _attend(q, cu, lens, table, kp, vp, ks, vs)
-    U.check_attend(o, lse, U.attend_plain(q, cu, lens, table, kp, vp, ks, vs))
-    assert _status(ws) == BOUNDS and _status(ws) == "STAR_OK"
+    want = U.attend_plain(q, cu, lens, table, kp, vp, ks, vs)
+    for tab, max_kv in ((table, 600), _wide(table, 16)):
+        o, lse, ws = _attend(q, cu, lens, tab, kp, vp, ks, vs, max_kv=max_kv)
+        U.check_attend(o, lse, want)
+        assert _status(ws) == BOUNDS and _status(ws) == "STAR_OK"
 
 
 @pytest.mark.parametrize("new", [1, 30])
 def test_attend_without_lse(new):
     lens = [700, 90]
-    q, cu, *rest = _attend_case(lens, [new, new], 8, 2, 64, 32, INT8, 25)
-    want, _, ws = _attend(q, cu, lens, *rest)
+    q, cu, table, *rest = _attend_case(lens, [new, new], 8, 2, 64, 32, INT8, 25)
+    table, max_kv = _wide(table, 32)
+    want, _, ws = _attend(q, cu, lens, table, *rest, max_kv=max_kv)
     o = torch.empty_like(want)
-    star.star_kv8_attend(q, ints(cu), ints(lens), *rest, o, ws, new, 700)
+    star.star_kv8_attend(q, ints(cu), ints(lens), table, *rest, o, ws, new, max_kv)
     assert torch.equal(o, want)
 
 
@@ -505,16 +525,17 @@ def test_attend_strides_padding_and_repeats(new):
     """q as heads of a fused buffer, padded rows untouched, and the same bits every time."""
     lens = [513, 40, 2000]
     q, cu, *rest = _attend_case(lens, new, 8, 2, 128, 64, E4M3, 29, pad=3)
+    rest[0], max_kv = _wide(rest[0], 64)
     n = q.shape[0]
     fused = torch.zeros(n, 12, 128, dtype=torch.bfloat16, device="cuda")
     fused[:, 2:10] = q
-    o, lse, ws = _attend(fused[:, 2:10], cu, lens, *rest, fill=5.0)
+    o, lse, ws = _attend(fused[:, 2:10], cu, lens, *rest, fill=5.0, max_kv=max_kv)
     wo, wl, ab, mag, low = U.attend_plain(q, cu, lens, *rest)
     m = cu[-1]
     U.check_attend(o[:m], lse[:, :m], (wo[:m], wl[:, :m], ab[:m], mag[:, :m], low[:m]))
     assert bool((o[cu[-1]:] == 5.0).all()) and bool((lse[:, cu[-1]:] == 5.0).all())
     for _ in range(5):
-        o2, lse2, _ = _attend(q, cu, lens, *rest, ws=ws, fill=5.0)
+        o2, lse2, _ = _attend(q, cu, lens, *rest, ws=ws, fill=5.0, max_kv=max_kv)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
@@ -548,9 +569,10 @@ def test_attend_one_workspace_for_calls_of_many_shapes():
     ws = star.alloc_workspace(star.star_kv8_attend_workspace_bytes(9, 200, 32, 8, 128, 100))
     for seed, (lens, new, *rest) in enumerate(shapes + shapes[::-1]):
         case = _attend_case(lens, new, *rest, 40 + seed)
-        a = _attend(case[0], case[1], lens, *case[2:], ws=ws)[:2]
-        b = _attend(case[0], case[1], lens, *case[2:])[:2]
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        for table, max_kv in ((case[2], max(lens)), _wide(case[2], rest[3])):
+            a = _attend(case[0], case[1], lens, table, *case[3:], ws=ws, max_kv=max_kv)[:2]
+            b = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)[:2]
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert _status(ws) == "STAR_OK"
 
 
@@ -589,7 +611,8 @@ def test_pools_beyond_32_bit_offsets(new):
         assert torch.equal(torch.where(rows, got[sub].double().cpu(), 0.0), torch.where(rows, want.values, 0.0))
     assert torch.equal(ks[sub].double().cpu(), sk) and torch.equal(vs[sub].double().cpu(), sv)
     q = torch.randn(new, 2 * h, d, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16).cuda()
-    o, lse, _ = _attend(q, [0, new], [n], ints([ids]), kp, vp, ks, vs)
+    table, max_kv = _wide(ints([ids]), page)
+    o, lse, _ = _attend(q, [0, new], [n], table, kp, vp, ks, vs, max_kv=max_kv)
     small = [t[sub].contiguous() for t in (kp, vp, ks, vs)]
     U.check_attend(o, lse, U.attend_plain(q, [0, new], [n], ints([[0, 1, 2]]), *small))
 
