@@ -3,8 +3,11 @@
 //
 // The mathematics is kv8_decode.cu's: s = ks_j (q . K) / sqrt(D), o = sum
 // e^(s - m) vs_j V / sum e^(s - m), token t of T seeing kv - T + t + 1 keys.
-// Bound: the exponential unit and the tensor cores, about equally (128 x 128
-// scores are 1024 cycles of either).
+// Bound: the exponential unit and the tensor cores, about equally (256 x 128
+// scores are 2048 cycles of either); what it spends now is the chain of one slot,
+// score products, softmax, weight products, about 5000 cycles a tile for both
+// slots out of step. 256 tokens of 64 heads after 128K keys of 8 heads (1.1
+// TFLOP): 1320 us, 833 TFLOP/s.
 //  * The T * g (token, query head) rows of a (request, KV head) are cut into
 //    tiles of 256 rows, two slots of 128: a K or V tile of 128 keys is read and
 //    converted once for both.
@@ -16,10 +19,15 @@
 //    fp16 (exact) in the 128-byte-swizzled layout that tcgen05.mma reads; K and V
 //    have the same layout. q is fp16 times a power of two per row, which keeps
 //    all its bits for elements down to 2^-29 of the row's largest.
-//  * Warps 0-3 and 4-7 own a slot each (thread = row = lane of tensor memory).
-//    MMA order per key tile: PV0(n), S0(n+1), PV1(n), S1(n+1), so that a slot's
-//    softmax runs beside the other's products. P (fp16) overwrites the first
-//    half of its S and feeds the P V product from tensor memory.
+//  * Eight warps own a slot: two threads for each row (lane of tensor memory), 64
+//    keys of a tile each. One warp issues a slot's products, PV(n) then S(n+1),
+//    the second slot's after the first's, so that a slot's softmax runs beside
+//    the other's products (in step, both slots contend for the exponential unit:
+//    1600 us). P (fp16) overwrites half of its S and feeds the P V product from
+//    tensor memory.
+//  * The roles' code competes for the instruction caches: a second copy of the
+//    softmax step for tiles whose V scales are equal, with a multiplication less,
+//    cost 70 us.
 //  * P is rounded to fp16 under 2^11 as in kv8_decode.cu, the running maximum
 //    moves when it grows by more than 2^4, and V scales enter through P as the
 //    ratio to a running reference that stays within [1, 2^12) of the tile's

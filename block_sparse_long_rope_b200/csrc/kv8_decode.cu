@@ -3,16 +3,19 @@
 // With codes K, V of page j and scales ks_j, vs_j, row r of a (request, KV head)
 // with query q sees
 //   s = ks_j (q . K) / sqrt(D),  o = sum e^(s - m) vs_j V / sum e^(s - m).
-// Bound: HBM, one byte an element of K and V. The design keeps that stream
-// going:
+// Bound: HBM, one byte an element of K and V: 1M tokens of 8 heads of 128 (2.15 GB)
+// take 333 us, 6.45 TB/s, where a loop that only copies takes 309; 16 requests of
+// 1K to 16K tokens (268 MB) 60 us, whose CTAs end between 40 and 60. A short call is
+// latency: 501 tokens of one head 7.6 us, of which one tile alone is 5.4. The design
+// keeps the stream going:
 //  * The T * g (token, query head) rows of a (request, KV head) form one tile of
 //    8 or 16 rows, so each code is read once for all of them; further rows make
 //    further tiles.
 //  * Work is cut by tiles of 128 keys: CTA c owns an equal contiguous range of
 //    the (request, head, row tile, key tile) list, whatever the lengths. Each
 //    CTA finds its range from the lengths itself. A CTA that holds a whole
-//    unit writes its output; parts of a unit go to the workspace, and the last
-//    CTA to finish one joins its parts in order.
+//    unit writes its output; parts of a unit go to the workspace, and the CTA
+//    that finishes one last joins its parts in order, once its own list is done.
 //  * Each of the 8 warps takes 16 keys of a tile and streams them through its
 //    own ring with cp.async, so nothing waits for other warps and pages need
 //    only be 16 rows. An instruction copies 512 contiguous bytes (64-byte pieces

@@ -17,7 +17,8 @@
 // walks over heads, its 8 cosines and sines in registers; the CTA builds them
 // once in shared memory, with their fp64 values for the slow path. The rounding
 // test takes both ends of the error interval as packed bf16 pairs and branches
-// once for a unit's 8 pairs.
+// once for a unit's 8 pairs. 16K tokens x 40 heads of 128 (336 MB): 61.9 us, 5.4
+// TB/s, two thirds of the issue slots; 16 tokens 3.0 us.
 #include <cmath>
 
 #include "kv8_kernels.cuh"

@@ -577,12 +577,16 @@ size_t star_kv8_attend_workspace_bytes(int B, int n_tokens, int Hq, int Hkv, int
  * 0, lse = -inf. Scale 1/sqrt(D); query head h uses KV head h / (Hq / Hkv).
  *   o [n_tokens, Hq, D] bf16, lse [Hq, n_tokens] fp32 (NULL to skip)
  * Rows from cu_new[B] on are left as they are, and so is what lies in pages
- * behind kv_len, which may hold anything. max_new bounds T, and max_kv
- * kv_len (1 .. max_pages * page_len): they choose kernels and grids, lengths
- * beyond them are an error. Each score is exact up to fp32 accumulation (q and
- * the codes enter the tensor cores unrounded); weights are rounded to 16 bits
- * before the product with V; sums and statistics are fp32. Results do not
- * depend on the order in which blocks run.
+ * behind kv_len, which may hold anything. o and lse overlap no input. max_new
+ * bounds T, and max_kv kv_len (1 .. max_pages * page_len): they choose kernels
+ * and grids, lengths beyond them are an error. Scores are fp32 sums of exact
+ * products (the codes enter the tensor cores unrounded, and so does q down to
+ * 2^-29 of its row's largest element). Weights, times the ratio of their V scale
+ * to one of up to 2^12 times the largest of 128 keys, are rounded to fp16 under
+ * 2^11: 11 bits of a weight down to 2^-25 of the largest, 2^-36 of the largest
+ * below that. Sums and statistics are fp32. A NaN code reaches only the rows
+ * that see its key. Results do not depend on the order in which blocks run. The
+ * workspace may serve calls of any smaller shapes too.
  * A request whose lengths or rows of q do not fit is left out, a page index
  * outside the pages makes its keys invisible; both record
  * STAR_ERR_DEVICE_BOUNDS.
