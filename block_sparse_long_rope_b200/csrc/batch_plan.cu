@@ -146,10 +146,7 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const __grid_const
 
   if (gridDim.x > 1) {
     __syncthreads();
-    if (tid == 0) {
-      __threadfence();
-      last = atomicInc(p.ticket, gridDim.x - 1) == gridDim.x - 1;
-    }
+    if (tid == 0) last = inc_acq_rel(p.ticket, gridDim.x - 1) == gridDim.x - 1;
     __syncthreads();
     if (!last) return;
   }

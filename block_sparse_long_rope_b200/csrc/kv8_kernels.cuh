@@ -11,6 +11,16 @@ namespace star {
 
 constexpr int kMaxRequests = 4096;  // requests of one call: their offsets live in shared memory
 
+#ifdef __CUDACC__
+// atomicInc that orders the block's work before it (after a barrier) and what the
+// thread does after it: one round trip to L2, where fences around it take another.
+__device__ __forceinline__ unsigned inc_acq_rel(unsigned* p, unsigned limit) {
+  unsigned old;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(limit) : "memory");
+  return old;
+}
+#endif
+
 // ---- rotary with given frequencies --------------------------------------------
 struct RopeScaledParams {
   const __nv_bfloat16* x;
