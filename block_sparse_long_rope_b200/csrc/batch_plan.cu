@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const __grid_const
   __shared__ Sums warp_sum[kWarps];
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  after_previous();
   const int P = 1 << p.page_shift;
   const long long limit = static_cast<long long>(p.max_pages) << p.page_shift;
 
@@ -172,8 +173,7 @@ cudaError_t launch_batch_plan(const BatchPlanParams& p, cudaStream_t stream) {
   // threads: 6.7 and 5.1 us). One CTA needs no ticket.
   const int most = imax(p.n_cap, p.run_cap);
   const int grid = imax(1, imin(148, ceil_div(most, kThreads)));
-  batch_plan_kernel<<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(batch_plan_kernel, dim3(grid), kThreads, smem, stream, p);
 }
 
 }  // namespace star

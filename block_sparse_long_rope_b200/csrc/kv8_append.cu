@@ -42,6 +42,7 @@ template <int kType, int D, int kVec>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const __grid_constant__ Kv8AppendParams p) {
   constexpr int kRowVecs = D / 8;  // 16-byte vectors of a bf16 row
   __shared__ uint32_t red[kThreads / 32];
+  after_previous();
   const int u = blockIdx.x, h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
   const int t0 = p.run_start[u], t1 = p.run_start[u + 1];
@@ -148,13 +149,12 @@ template <int kType, int D>
 cudaError_t launch_type(const Kv8AppendParams& p, cudaStream_t stream) {
   const dim3 grid(p.run_cap, p.Hkv, 2);
   switch ((D << p.page_shift) / 8 / kThreads) {  // vectors of a thread for a full page
-    case 1: kv8_append_kernel<kType, D, 1><<<grid, kThreads, 0, stream>>>(p); break;
-    case 2: kv8_append_kernel<kType, D, 2><<<grid, kThreads, 0, stream>>>(p); break;
-    case 4: kv8_append_kernel<kType, D, 4><<<grid, kThreads, 0, stream>>>(p); break;
-    case 8: kv8_append_kernel<kType, D, 8><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv8_append_kernel<kType, D, 16><<<grid, kThreads, 0, stream>>>(p); break;
+    case 1: return launch_after(kv8_append_kernel<kType, D, 1>, grid, kThreads, 0, stream, p);
+    case 2: return launch_after(kv8_append_kernel<kType, D, 2>, grid, kThreads, 0, stream, p);
+    case 4: return launch_after(kv8_append_kernel<kType, D, 4>, grid, kThreads, 0, stream, p);
+    case 8: return launch_after(kv8_append_kernel<kType, D, 8>, grid, kThreads, 0, stream, p);
+    default: return launch_after(kv8_append_kernel<kType, D, 16>, grid, kThreads, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   __shared__ uint32_t row_q[2][2][128];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  after_previous();
   // the join may be launched where there is room: it waits for this kernel's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -865,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ Kv8AttendParams p) {
   extern __shared__ int prefix[];
-  // (the lengths were there before the attention began)
+  // (the lengths were there before the attention let this kernel begin)
   tiles_before(p, prefix, kJoinThreads);
   __syncthreads();
   const int total = prefix[p.B], G = imin(static_cast<int>(gridDim.x), total);
@@ -883,7 +884,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   }
   // the parts are there; every block waits, so that what follows this kernel
   // also follows the attention
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   if (rows <= 0) return;
   // CTA of list index x: the largest c with floor(c * total / G) <= x
   const int c1 = static_cast<int>(((last_tile + 1) * G - 1) / total);
@@ -960,21 +961,10 @@ cudaError_t launch(const Kv8AttendParams& p, int slot, int sms, cudaStream_t str
                                            Cfg<D>::bytes(kMaxRequests));
   if (e != cudaSuccess) return e;
   const int grid = imin(kKv8ChunkMaxCtas, sms);
-  kv8_chunk_kernel<D, kType><<<grid, kThreads, Cfg<D>::bytes(p.B), stream>>>(p);
-  const cudaError_t launched = cudaGetLastError();
+  const cudaError_t launched =
+      launch_after(kv8_chunk_kernel<D, kType>, dim3(grid), kThreads, Cfg<D>::bytes(p.B), stream, p);
   if (launched != cudaSuccess) return launched;
-  // the join's launch overlaps the end of the attention
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, kRows / 32);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = (p.B + 1) * sizeof(int);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv8_join_kernel<D>, p);
+  return launch_after(kv8_join_kernel<D>, dim3(grid, kRows / 32), kJoinThreads, (p.B + 1) * sizeof(int), stream, p);
 }
 }  // namespace
 

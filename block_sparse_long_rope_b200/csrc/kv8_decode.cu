@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
   const int gq = lane >> 2, t4 = lane & 3;
   const int P = 1 << p.page_shift;
 
+  after_previous();
   // ---- tiles before each request
   {
     const int per = ceil_div(p.B, kThreads);
@@ -723,8 +724,7 @@ cudaError_t launch(const Kv8AttendParams& p, int sms, cudaStream_t stream) {
     if (dev >= 0 && dev < 64) raised[dev].store(true, std::memory_order_release);
   }
   const int grid = imin(kKv8MaxCtas, ctas_per_sm(D, NT) * sms);
-  kv8_decode_kernel<D, kType, NT><<<grid, kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(kv8_decode_kernel<D, kType, NT>, dim3(grid), kThreads, smem, stream, p);
 }
 }  // namespace
 

@@ -53,6 +53,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
   __shared__ double2 exact[kMaxTok][64];  // m (cos, sin)
   // their fp32 roundings, 8 pairs of a unit and a gap: units lie in other banks
   __shared__ float2 tab[kMaxTok][kUnits * 10];
+  after_previous();
   const int half = p.rot / 2;
   const int tok0 = blockIdx.x * p.tpc, ntok = imin(p.tpc, p.S - tok0);
   const int b = blockIdx.y;
@@ -169,18 +170,11 @@ cudaError_t launch_rope_scaled(const RopeScaledParams& p_in, bool interleaved, c
   while (p.tpc > 1 && (long long)ceil_div(p.S, p.tpc) * p.B < 2 * 148) p.tpc /= 2;
   p.hpc = (long long)ceil_div(p.S, p.tpc) * p.B < 148 ? imin(p.H, groups / p.tpc) : p.H;
   const dim3 grid(ceil_div(p.S, p.tpc), p.B, ceil_div(p.H, p.hpc));
-  if (p.D == 128) {
-    if (interleaved)
-      rope_scaled_kernel<128, true><<<grid, kThreads, 0, stream>>>(p);
-    else
-      rope_scaled_kernel<128, false><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved)
-      rope_scaled_kernel<64, true><<<grid, kThreads, 0, stream>>>(p);
-    else
-      rope_scaled_kernel<64, false><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  if (p.D == 128)
+    return interleaved ? launch_after(rope_scaled_kernel<128, true>, grid, kThreads, 0, stream, p)
+                       : launch_after(rope_scaled_kernel<128, false>, grid, kThreads, 0, stream, p);
+  return interleaved ? launch_after(rope_scaled_kernel<64, true>, grid, kThreads, 0, stream, p)
+                     : launch_after(rope_scaled_kernel<64, false>, grid, kThreads, 0, stream, p);
 }
 
 }  // namespace star
