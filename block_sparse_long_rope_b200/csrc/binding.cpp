@@ -1,6 +1,6 @@
 // Native half of the torch binding for the calls of a serving step, which are
 // short enough that checking their tensors from Python would take longer than
-// the kernels (16 to 21 us a call; 4 to 5 us from here). star.py holds the
+// the kernels (16 to 21 us a call; 3.7 to 4 us from here). star.py holds the
 // public functions; these take their arguments in order, check them, make the
 // tensors' device current and call the C ABI of the libstar.so that bind() was
 // given. They return its status, which star.py turns into an error.
