@@ -692,13 +692,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
       float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f, fs = next_fs;
       bool nan = false;
-      for (int i = 0; i < seg; ++i) {
+      // A slot without rows skips the tiles: nobody would hold the ring for it. Rounds of
+      // the ring may have passed since its last tile, and a wait by parity takes only
+      // one for its own, so a segment begins with the wait for its first scores: they
+      // are there after the tile's scales, and no later round is until P answers them.
+      if (active) ok &= warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status);
+      for (int i = 0; active && i < seg; ++i) {
         const int n = n0 + i;
         const Scales& ss = ring[n % kRing];
-        // (a slot without rows still follows the ring: its next wait would otherwise
-        // mistake an earlier round for its own)
         ok &= warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status);
-        if (!active) continue;
         const int key0 = (here.tile + i) * kKv8Tile, seen = limit - key0 - 64 * half;
         float kmin = ss.k[0], vmax = ss.v[0];
 #pragma unroll
