@@ -31,8 +31,8 @@
 //  * P is rounded to fp16 under 2^11 as in kv8_decode.cu, the running maximum
 //    moves when it grows by more than 2^4, and V scales enter through P as the
 //    ratio to a running reference that stays within [1, 2^12) of the tile's
-//    largest. Values whose scale is 2^24 below the largest of their 128 keys
-//    lose bits.
+//    largest, or 2^64 below the largest so far (see next_reference). Values whose
+//    scale is 2^24 below the largest of their 128 keys lose bits.
 #include <math.h>
 
 #include "kv8_codes.cuh"
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   // what a row's two threads exchange
   __shared__ float row_l[2][2][128], row_m[2][2][2][128];
   __shared__ uint32_t row_q[2][2][128];
+  __shared__ float v_top[16];  // by softmax warp
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   after_previous();
@@ -749,11 +750,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
           l *= alpha;
           if (new_vref) {
-            alpha *= vref / vmax;
-            vref = vmax;
-            ivref = 1.f / vmax;
+            const float to = next_reference(vref, vmax, &v_top[warp]);
+            alpha *= vref / to;
+            vref = to;
+            ivref = 1.f / to;
           }
-          if (i > 0) {
+          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
             for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
               uint32_t r[16];

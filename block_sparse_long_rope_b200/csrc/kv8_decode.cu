@@ -33,7 +33,7 @@
 //    tail behind one peak still adds up. The running maximum moves only when
 //    it grows by more than 2^4, so P < 2^15 stays finite.
 //  * V scales enter through P as the ratio to a running reference; beyond
-//    [2^-12, 1] the reference moves and O is rescaled.
+//    [2^-12, 1] the reference moves and O is rescaled (see next_reference).
 #include <math.h>
 
 #include <atomic>
@@ -165,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
   int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);  // [B + 1] tiles before request b
   __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
   __shared__ int warp_tiles[kWarps];
+  __shared__ float v_top[kWarps];
   __shared__ Cut cuts[2];
   int ncuts = 0;
 
@@ -438,15 +439,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         // ---- the V scale as a ratio to the reference
         const float vs = *static_cast<const volatile float*>(scales + 2 * stage + 1);
         if (vs > vref || (vs < vref * 0.000244140625f && vs > 0.f)) {
-          const float a = vref / vs;
+          const float to = next_reference(vref, vs, &v_top[warp]);
+          if (to != vref) {
+            const float a = vref / to;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j)
+              for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) o[nt][j][c] *= a;
-          vref = vs;
-          inv_vref = 1.f / vs;
+                for (int c = 0; c < 4; ++c) o[nt][j][c] *= a;
+            vref = to;
+            inv_vref = 1.f / to;
+          }
         }
         const float vr = vs * inv_vref;
         // ---- P^T, by columns of keys

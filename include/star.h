@@ -582,11 +582,12 @@ size_t star_kv8_attend_workspace_bytes(int B, int n_tokens, int Hq, int Hkv, int
  * and grids, lengths beyond them are an error. Scores are fp32 sums of exact
  * products (the codes enter the tensor cores unrounded, and so does q down to
  * 2^-29 of its row's largest element). Weights, times the ratio of their V scale
- * to one of up to 2^12 times the largest of 128 keys, are rounded to fp16 under
- * 2^11: 11 bits of a weight down to 2^-25 of the largest, 2^-36 of the largest
- * below that. Sums and statistics are fp32. A NaN code reaches only the rows
- * that see its key. Results do not depend on the order in which blocks run. The
- * workspace may serve calls of any smaller shapes too.
+ * to a reference, are rounded to fp16 under 2^11: 11 bits of a weight down to
+ * 2^-25 of the largest, 2^-36 of the largest below that. The reference is at most
+ * 2^12 times the largest scale of 128 keys, or 2^-64 of the request's largest.
+ * Sums and statistics are fp32. A NaN code reaches only the rows that see its
+ * key. Results do not depend on the order in which blocks run. The workspace may
+ * serve calls of any smaller shapes too.
  * A request whose lengths or rows of q do not fit is left out, a page index
  * outside the pages makes its keys invisible; both record
  * STAR_ERR_DEVICE_BOUNDS.

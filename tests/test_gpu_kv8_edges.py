@@ -37,3 +37,69 @@ def test_attend_slots_without_rows_behind_slow_ends(D, page, g):
         assert _status(ws) == "STAR_OK"
         assert torch.equal(torch.isnan(o), hit) and torch.equal(lse, lse0)
         assert torch.equal(o[~hit], clean[~hit])
+
+
+# ---- V scales over the whole range -----------------------------------------------------------------
+def _reach(cu, kv, table, kp, vp, vs):
+    """What the floor of the reference adds to `low` of check_attend: the reference stays within 2^-64 of the
+    request's largest V scale, so each key may be off by 2^-36 |code| times that."""
+    P, Hkv, page, D = kp.shape
+    out = []
+    for b, L in enumerate(kv):
+        ids = table[b, :-(-L // page)].long()
+        top = vs[ids].double().amax(0) * 2.0 ** -64  # [Hkv]
+        code = vp[ids].double().nan_to_num().abs().sum((0, 2)) * top[:, None]
+        out.append(code[None].expand(cu[b + 1] - cu[b], Hkv, D))
+    return torch.cat(out)
+
+
+def _check_scales(lens, new, case, tables):
+    q, cu, _, kp, vp, ks, vs = case
+    for table, max_kv in tables:
+        wo, wl, ab, mag, low = U.attend_plain(q, cu, lens, table, kp, vp, ks, vs)
+        more = _reach(cu, lens, table, kp, vp, vs).repeat_interleave(q.shape[1] // kp.shape[1], 1)
+        o, lse, ws = _attend(q, cu, lens, table, kp, vp, ks, vs, max_kv=max_kv)
+        U.check_attend(o, lse, (wo, wl, ab, mag, low + more))
+        assert _status(ws) == "STAR_OK"
+
+
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("big,tiny", [(12, -100), (70, -70), (50, -60), (0, -100), (60, -126)])
+@pytest.mark.parametrize("order", ["big tiny big", "tiny big tiny", "big tiny tiny"])
+def test_attend_scales_far_apart(kind, new, big, tiny, order):
+    """V scales 2^60 to 2^186 apart in every order, in spans of whole tiles and of single pages."""
+    lens, page = [3000, 1300], 64
+    case = list(_attend_case(lens, [new, new], 8, 2, 128, page, kind, 83))
+    table, vs = case[2], case[6]
+    for b, L in enumerate(lens):
+        n = -(-L // page)
+        for j in range(n):
+            word = order.split()[min(2, 3 * j // n)]
+            if b == 1:  # pages take turns: both within one tile
+                word = order.split()[j % 3]
+            vs[int(table[b, j])] = 2.0 ** (big if word == "big" else tiny)
+    _check_scales(lens, [new, new], case, [(table, 3000), _wide(table, page)])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attend_zero_pages_from_append(new):
+    """Pages of zeros as star_kv8_append writes them (scale 2^-100) behind a long flat context and before more of
+    it: the outputs stay finite and right."""
+    page, h, d, L, kind = 64, 2, 64, 200000, E4M3
+    n = -(-L // page)
+    kp, ks = U.make_pages(n, h, page, d, kind, 91)
+    vp, vs = U.make_pages(n, h, page, d, kind, 92)
+    ks.mul_(2.0 ** -12)  # nearly equal weights
+    vs.mul_(2.0 ** 20)
+    zero = list(range(0, n, 7)) + list(range(n // 2, n // 2 + 40))
+    x = torch.zeros(page * len(zero), h, d, dtype=torch.bfloat16, device="cuda")
+    slots = [p * page + r for p in zero for r in range(page)]
+    ws = star.alloc_workspace(256)
+    star.star_kv8_append(x, x, ints(slots), ints([i * page for i in range(len(zero) + 1)]), kp, vp, ks, vs, ws)
+    assert _status(ws) == "STAR_OK" and bool((vs[zero] == 2.0 ** -100).all())
+    q = torch.randn(new, 4, d, generator=torch.Generator().manual_seed(93)).to(torch.bfloat16).cuda()
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(94)).to(torch.int32).cuda()[None]
+    ordered = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    for t in (table, ordered):
+        _check_scales([L], [new], (q, [0, new], t, kp, vp, ks, vs), [(t, L)])
