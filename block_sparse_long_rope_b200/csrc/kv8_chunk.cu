@@ -811,13 +811,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         const bool valid = ok && 128 * x + row < rows;
         const int head = here.kvh * p.g + my_row % p.g;
         const size_t token = here.r.q0 + my_row / p.g;
-        const float mul = whole ? (l != 0.f ? vref / l : 0.f) : vref;
+        const float mul = whole ? (l != 0.f ? 1.f / l : 0.f) : kKv8Join;
         for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {
           uint32_t r[32];
           __syncwarp();
           tmem_ld32_now(tO + 32 * q, r);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * mul);
+          for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * mul * vref);
           if (!valid) continue;
           if (nan) {
             const int key0 = imax(here.tile * kKv8Tile, unit_lo / kKv8Tile * kKv8Tile);
@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
               l != 0.f ? (rf + log2f(l)) * 0.6931471805599453f : -INFINITY;
         if (valid && !whole && half == 0)  // nothing seen (or only NaN): a reference of -inf
           *reinterpret_cast<float2*>(p.part_ml + 2 * (part * kRows + 128 * x + row)) =
-              make_float2(m == -INFINITY ? -INFINITY : rf, l);
+              make_float2(m == -INFINITY ? -INFINITY : rf, l * kKv8Join);
         tc_fence_before();
       }
     }
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + 4 * v) = y;
     if (v == 0 && p.lse)
       p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-          L[i] != 0.f ? (M[i] + log2f(L[i])) * 0.6931471805599453f : -INFINITY;
+          L[i] != 0.f ? (M[i] + kKv8JoinShift + log2f(L[i])) * 0.6931471805599453f : -INFINITY;
   }
 }
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ void finish_row(const Kv8AttendParams& p, const Cut& 
   *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
   if (d == 0 && p.lse)
     p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-        L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+        L != 0.f ? (M + (kKv8JoinShift - kPShift) + log2f(L)) * 0.6931471805599453f : -INFINITY;
 }
 
 }  // namespace
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         float M = -INFINITY;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) M = fmaxf(M, wm[x][8 * nt + 2 * t4 + c]);
-        w[c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * vref;
+        w[c] = M == -INFINITY ? 0.f : ex2_approx(m[nt][c] - M) * kKv8Join;
       }
       float* mine = reinterpret_cast<float*>(ring + free_stage * C::kStage);  // [8][D]
 #pragma unroll
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           *reinterpret_cast<float2*>(mine + (2 * t4 + c) * D + gq * (D / 8) + 2 * j) =
-              make_float2(o[nt][j][c] * w[c], o[nt][j][c + 2] * w[c]);
+              make_float2(o[nt][j][c] * w[c] * vref, o[nt][j][c + 2] * w[c] * vref);
       __syncthreads();
       const int n = tid / (D / 4), d = 4 * (tid % (D / 4));
       if (n < 8) {
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
               reinterpret_cast<const float*>(smem + x * C::kRing + free_stage * C::kStage) + n * D + d);
           sum = make_float4(sum.x + y.x, sum.y + y.y, sum.z + y.z, sum.w + y.w);
           // (a maximum of -inf: nothing seen, a sum of 0, or only NaN)
-          L += M == -INFINITY ? wl[x][8 * nt + n] : wl[x][8 * nt + n] * ex2_approx(wm[x][8 * nt + n] - M);
+          L += M == -INFINITY ? wl[x][8 * nt + n] : wl[x][8 * nt + n] * kKv8Join * ex2_approx(wm[x][8 * nt + n] - M);
         }
         if (8 * nt + n < rows) {
           if (whole) {
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
             *reinterpret_cast<uint2*>(p.o + (token * p.Hq + head) * D + d) = y;
             if (d == 0 && p.lse)
               p.lse[static_cast<size_t>(head) * p.n_tokens + token] =
-                  L != 0.f ? (M - kPShift + log2f(L)) * 0.6931471805599453f : -INFINITY;
+                  L != 0.f ? (M + (kKv8JoinShift - kPShift) + log2f(L)) * 0.6931471805599453f : -INFINITY;
           } else {
             *reinterpret_cast<float4*>(p.part_o + (part * kRows + 8 * nt + n) * D + d) = sum;
             if (d == 0)

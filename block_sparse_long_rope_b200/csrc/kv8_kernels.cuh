@@ -111,6 +111,10 @@ struct Kv8AttendParams {
   float* part_o;        // [CTAs][2][rows][D] ([D / 4][rows][4] of the chunk kernel)
 };
 constexpr int kKv8Tile = 128;     // keys of one tile of a CTA
+// Sums that are joined, of weights and of weighted values, are held times 2^-20: P is up
+// to 2^15, and 2^15 times values near the largest number do not fit fp32 where their
+// average does. (The weights' sum is at least 2^-20 then, and usually 2^-9.)
+constexpr float kKv8JoinShift = 20.f, kKv8Join = 9.5367431640625e-07f;
 constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many (decode)
 constexpr int kKv8ChunkRows = 256, kKv8ChunkMaxCtas = 160;
 // Rows of a (request, KV head) tile: 8 or 16 of the decode kernel, or the chunk

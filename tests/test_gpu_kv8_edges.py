@@ -103,3 +103,39 @@ def test_attend_zero_pages_from_append(new):
     ordered = torch.arange(n, dtype=torch.int32, device="cuda")[None]
     for t in (table, ordered):
         _check_scales([L], [new], (q, [0, new], t, kp, vp, ks, vs), [(t, L)])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_attend_largest_values(kind, new):
+    """Values near the largest bf16 number over a long context: a sum of weights under 2^11 times them does
+    not fit fp32, their average does."""
+    lens, page = [20000, 17], 32
+    case = list(_attend_case(lens, [new, new], 4, 1, 64, page, kind, 97, spread=0.0))
+    case[6] *= 2.0 ** 116
+    want = U.attend_plain(case[0], case[1], lens, *case[2:])
+    assert torch.isfinite(want[0].float()).all() and float(want[0].abs().max()) > 2.0 ** 110
+    for table, max_kv in ((case[2], 20000), _wide(case[2], page)):
+        o, lse, _ = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)
+        U.check_attend(o, lse, want)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [1.0, 1.37])
+def test_attend_smallest_scales(scale, new):
+    """The other end: V scales of 2^-126, the smallest normal numbers."""
+    lens, page = [20000, 17], 32
+    case = list(_attend_case(lens, [new, new], 4, 1, 64, page, INT8, 98, spread=0.0))
+    case[6].fill_(scale * 2.0 ** -126)
+    case[4].clamp_(-40, 70).add_(50)  # values of one sign: the average is as large as they are
+    wo, wl, ab, mag, low = U.attend_plain(case[0], case[1], lens, *case[2:])
+    for table, max_kv in ((case[2], 20000), _wide(case[2], page)):
+        o, lse, _ = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)
+        # (o in units of 2^-126: check_attend's absolute term is far above them)
+        err = (o.double() - wo).abs() * 2.0 ** 126
+        ds = 16 * 2.0 ** -23 * mag.T.unsqueeze(-1)
+        # and half of fp32's fixed step of 2^-149 from each of 8 warps of up to 300 parts, over a sum of weights
+        # of 2^-9 at least
+        bound = (2.0 ** -8 * wo + ab * (2.0 ** -11 + 2.0 ** -18 + 2 * ds)) * 2.0 ** 126 + 2400 * 2.0 ** -15
+        assert bool((err <= bound).all())
+        assert float(wo[~torch.isinf(wl.T)].min()) > 2.0 ** -126  # (the second request's first rows see no key)
