@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   // what a row's two threads exchange
   __shared__ float row_l[2][2][128], row_m[2][2][2][128];
   __shared__ uint32_t row_q[2][2][128];
-  __shared__ float v_top[16];  // by softmax warp
+  __shared__ float v_top[512];  // largest V scale so far, by softmax thread (a register more spills)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   after_previous();
@@ -698,7 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // one for its own, so a segment begins with the wait for its first scores: they
       // are there after the tile's scales, and no later round is until P answers them.
       if (active) ok &= warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status);
-      for (int i = 0; active && i < seg; ++i) {
+      if (active)  // (a loop of its own: with the test in its condition the kernel takes 2% longer)
+#pragma unroll 1
+      for (int i = 0; i < seg; ++i) {
         const int n = n0 + i;
         const Scales& ss = ring[n % kRing];
         ok &= warp_wait(&sc_full[n % kRing], (n / kRing) & 1, &abort_flag, p.status);
@@ -750,12 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           }
           l *= alpha;
           if (new_vref) {
-            const float to = next_reference(vref, vmax, &v_top[warp]);
+            const float top = vref > 0.f ? fmaxf(v_top[tid], vmax) : vmax, to = next_reference(vmax, top);
+            v_top[tid] = top;
             alpha *= vref / to;
             vref = to;
             ivref = 1.f / to;
           }
-          if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          if (i > 0) {
 #pragma unroll 1
             for (int q = half * (D / 32); q < (half + 1) * (D / 32); ++q) {
               uint32_t r[16];
@@ -813,16 +816,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         const size_t token = here.r.q0 + my_row / p.g;
         const float mul = whole ? (l != 0.f ? 1.f / l : 0.f) : kKv8Join;
         for (int q = half * (D / 64); q < (half + 1) * (D / 64); ++q) {
+          uint32_t bits = 0;
+          if (nan && valid) {  // (before the load: its registers would be saved for the call)
+            const int key0 = imax(here.tile * kKv8Tile, unit_lo / kKv8Tile * kKv8Tile);
+            bits = nan_columns<D>(p, here.b, here.kvh, key0, imin(limit, (here.tile + seg) * kKv8Tile), q);
+          }
           uint32_t r[32];
           __syncwarp();
           tmem_ld32_now(tO + 32 * q, r);
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * mul * vref);
           if (!valid) continue;
-          if (nan) {
-            const int key0 = imax(here.tile * kKv8Tile, unit_lo / kKv8Tile * kKv8Tile);
-            const uint32_t bits = nan_columns<D>(p, here.b, here.kvh, key0,
-                                                 imin(limit, (here.tile + seg) * kKv8Tile), q);
+          if (bits) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if ((bits >> j) & 1u) r[j] = 0x7FFFFFFFu;

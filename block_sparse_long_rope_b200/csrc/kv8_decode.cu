@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
   int* prefix = reinterpret_cast<int*>(smem + C::kPrefix);  // [B + 1] tiles before request b
   __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
   __shared__ int warp_tiles[kWarps];
-  __shared__ float v_top[kWarps];
+  __shared__ float v_top[kWarps];  // largest V scale so far (a register more spills)
   __shared__ Cut cuts[2];
   int ncuts = 0;
 
@@ -439,7 +439,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
         // ---- the V scale as a ratio to the reference
         const float vs = *static_cast<const volatile float*>(scales + 2 * stage + 1);
         if (vs > vref || (vs < vref * 0.000244140625f && vs > 0.f)) {
-          const float to = next_reference(vref, vs, &v_top[warp]);
+          const float top = vref > 0.f ? fmaxf(v_top[warp], vs) : vs, to = next_reference(vs, top);
+          __syncwarp();
+          if (lane == 0) v_top[warp] = top;
+          __syncwarp();
           if (to != vref) {
             const float a = vref / to;
 #pragma unroll

@@ -23,16 +23,12 @@ __device__ __forceinline__ unsigned inc_acq_rel(unsigned* p, unsigned limit) {
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Where the attention kernels' reference of V scales goes when vs, the largest scale at
-// hand, is above it or 2^12 below it: to vs, but no further than 2^64 below *top, the
-// largest so far (a warp's own word, set anew where ref is 0: before the first). O is held
-// in units of the reference: at most 2^24 for each of 2^31 keys times 2^64, it stays
-// finite whatever scales follow one another (star_kv8_append gives a page of zeros 2^-100).
-__device__ __forceinline__ float next_reference(float ref, float vs, float* top) {
-  const float t = ref > 0.f ? fmaxf(*top, vs) : vs;
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) *top = t;
-  __syncwarp();
-  return fmaxf(vs, t * 5.421010862427522e-20f);
+// hand, is above it or 2^12 below it: to vs, but no further than 2^64 below top, the
+// largest so far. O is held in units of the reference: at most 2^24 for each of 2^31
+// keys times 2^64, it stays finite whatever scales follow one another (star_kv8_append
+// gives a page of zeros 2^-100).
+__device__ __forceinline__ float next_reference(float vs, float top) {
+  return fmaxf(vs, top * 5.421010862427522e-20f);
 }
 #endif
 
