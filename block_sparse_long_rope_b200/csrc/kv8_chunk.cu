@@ -51,6 +51,11 @@ constexpr int kRows = kKv8ChunkRows;
 constexpr int kRing = 8;       // tiles whose scales are kept: more than the stages ahead
 constexpr float kShift = 11.f; // P is held as 2^11 e^(s - m)
 constexpr float kSlack = 4.f;  // growth of the maximum (log2) before it moves
+// s_j f - rf in one rounding may lie half a step of the maximum above what the rounded
+// maximum allows, or below: 2^-9 up to here, but 16 at 2^28, where P leaves fp16. Rows
+// beyond it round s_j f first, as the maximum's product was (for all rows that costs
+// 80 us of 1410).
+constexpr float kFar = 65536.f;
 
 template <int D>
 struct Cfg {
@@ -271,8 +276,8 @@ __device__ __forceinline__ void tmem_ld32_now(uint32_t taddr, uint32_t (&s)[32])
 
 // Steps of the softmax over 32 of a row's scores s. Score j in log2 units is
 // s_j f, f = fs ks for the two groups of 16 keys.
-// At an edge: scaled scores, with -inf for keys from `seen` on and for those of
-// missing pages (ks < 0); f is 1 from then on.
+// At an edge, or beyond kFar: scaled scores, with -inf for keys from `seen` on and for
+// those of missing pages (ks < 0); f is 1 from then on.
 __device__ __forceinline__ void mask_32(uint32_t (&s)[32], const float* ks, float fs, int seen) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
@@ -688,8 +693,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       const bool active = x == 0 || rows > 128;
       const int my_row = here.rt * kRows + 128 * x + row;
       const int limit = keys_of_row(p, here.r, my_row);
-      // keys that the slot's and the unit's first rows see
-      const int lim_lo = keys_of_row(p, here.r, here.rt * kRows + 128 * x);
+      // keys that the slot's and the unit's first rows see; the former's tiles need no
+      // mask (0 once a row is beyond kFar: none do without)
+      int lim_lo = keys_of_row(p, here.r, here.rt * kRows + 128 * x);
       const int unit_lo = keys_of_row(p, here.r, here.rt * kRows);
       float m = -INFINITY, rf = 0.f, l = 0.f, vref = 0.f, ivref = 0.f, fs = next_fs;
       bool nan = false;
@@ -711,15 +717,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           kmin = fminf(kmin, ss.k[j]);
           vmax = fmaxf(vmax, ss.v[j]);
         }
-        const bool masked = key0 + kKv8Tile > lim_lo || kmin < 0.f;
+        bool masked = key0 + kKv8Tile > lim_lo || kmin < 0.f;
         const bool new_vref = vmax > vref || (vmax < vref * 0.000244140625f && vmax > 0.f);
         const float *ks = ss.k + 4 * half, *vs = ss.v + 4 * half;
         auto factor = [&](int g) { return masked ? 1.f : fs * ks[g]; };
 
         ok &= warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status);
         tc_fence_after();
-        // ---- row maximum in log2 units, 32 scores at a time; the last 32 stay (loops
-        // that are not unrolled: the roles share small instruction caches)
+        // ---- row maximum in log2 units, 32 scores at a time (loops that are not unrolled:
+        // the roles share small instruction caches; scores that stay in registers until
+        // P would spill others)
         uint32_t s[32];
         float mt = -INFINITY;
 #pragma unroll 1
@@ -750,6 +757,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
             alpha = none ? 1.f : ex2_approx(rf - nrf);
             rf = nrf;
           }
+          if (__any_sync(0xffffffffu, fabsf(rf) > kFar)) {
+            masked = true;
+            lim_lo = 0;
+          }
           l *= alpha;
           if (new_vref) {
             const float top = vref > 0.f ? fmaxf(v_top[tid], vmax) : vmax, to = next_reference(vmax, top);
@@ -772,16 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
             tmem_wait_st();
           }
         }
-        // ---- P over S: the 32 scores at hand into the columns that they came from,
-        // then the others
+        // ---- P over S: the upper 32 scores' into the columns that they came from, then
+        // the others'
         const uint64_t nref = f2_pack(-rf, -rf);
         uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int q = 1; q >= 0; --q) {
-          if (q == 0) {
-            tmem_ld32_now(tS, s);
-            if (masked) mask_32(s, ks, fs, seen);
-          }
+          tmem_ld32_now(tS + 32 * q, s);
+          if (masked) mask_32(s, ks + 2 * q, fs, seen - 32 * q);
           const float f0 = factor(2 * q), f1 = factor(2 * q + 1);
           const uint32_t dst = tS + (q ? 32 : 48);
           p_32(s, f0, f1, vs[2 * q] * ivref, vs[2 * q + 1] * ivref, nref, ls, dst);

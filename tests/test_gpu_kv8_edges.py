@@ -139,3 +139,35 @@ def test_attend_smallest_scales(scale, new):
         bound = (2.0 ** -8 * wo + ab * (2.0 ** -11 + 2.0 ** -18 + 2 * ds)) * 2.0 ** 126 + 2400 * 2.0 ** -15
         assert bool((err <= bound).all())
         assert float(wo[~torch.isinf(wl.T)].min()) > 2.0 ** -126  # (the second request's first rows see no key)
+
+
+# ---- scores so large that fp32 steps over whole numbers ----------------------------------------------
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("size", [0, 10, 14, 20])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attend_huge_scores(new, size, sign):
+    """Scores of up to 2^40 of either sign, one key ahead of the others by more than any rounding: its value in
+    bf16 is the output. Rows differ in size, so that their maxima are rounded differently."""
+    L, D, page, Hq = 5000, 64, 16, 8
+    n, best = -(-L // page), 2345
+    g = torch.Generator().manual_seed(101)
+    flip = torch.randint(0, 2, (D,), generator=g) * 2 - 1
+    # q . K is between 100 and 127 of D |q|'s for the others where it is negative, within 20 of them where not
+    other = torch.randint(-20, 21, (n, 1, page, D), generator=g) if sign > 0 else \
+        -flip * torch.randint(100, 128, (n, 1, page, D), generator=g)
+    kp = other.to(INT8)
+    kp[best // page, 0, best % page] = ((127 if sign > 0 else -60) * flip).to(INT8)
+    vp = torch.randint(-127, 128, (n, 1, page, D), generator=g).to(INT8).cuda()
+    rows = (1 + torch.arange(new * Hq) / (new * Hq)) * 2.0 ** (8 + size)
+    q = (rows[:, None] * flip[None]).to(torch.bfloat16).view(new, Hq, D).cuda()
+    one = torch.ones(n, 1, device="cuda")
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    want = vp[best // page, 0, best % page].to(torch.bfloat16)
+    for t, max_kv in ((table, L), _wide(table, page)):
+        o, lse, ws = _attend(q, [0, new], [L], t, kp.cuda(), vp, one, one, max_kv=max_kv)
+        assert _status(ws) == "STAR_OK"
+        assert torch.equal(o, want.expand_as(o))
+        # (D products of at most 8 and 7 bits and their sum are exact; one rounding each for the factor, the
+        # score and the logarithm's)
+        score = q.double().abs().sum(2).T * (127 if sign > 0 else -60) / math.sqrt(D)
+        assert bool(((lse.double() - score).abs() <= 2.0 ** -21 * (score.abs() + 8)).all())
