@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           nan |= (flags.x | flags.y | flags.z | flags.w) != 0;
         }
         // ---- now and then the maximum and the V reference move; O and the sum follow
-        const bool up = mt > m + kSlack;
+        const bool up = mt > __fadd_rd(m, kSlack);  // (rounded up, a step of 8 would pass)
         if (new_vref || __any_sync(0xffffffffu, up)) {
           float alpha = 1.f;
           if (up) {

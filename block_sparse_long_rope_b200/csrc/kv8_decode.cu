@@ -410,12 +410,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
               if (key >= past + r / p.g) s[nt][c] = -INFINITY;
             }
         }
-        // ---- running maximum, moved only when it grows by more than kSlack
+        // ---- running maximum, moved only when it grows by more than kSlack (the sum
+        // rounded down: near 2^26 a maximum moves in steps of 8, and up is 8)
         bool grow = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) grow |= s[nt][c] > m[nt][c & 1] + kSlack;
+          for (int c = 0; c < 4; ++c) grow |= s[nt][c] > __fadd_rd(m[nt][c & 1], kSlack);
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)

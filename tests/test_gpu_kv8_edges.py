@@ -171,3 +171,28 @@ def test_attend_huge_scores(new, size, sign):
         # score and the logarithm's)
         score = q.double().abs().sum(2).T * (127 if sign > 0 else -60) / math.sqrt(D)
         assert bool(((lse.double() - score).abs() <= 2.0 ** -21 * (score.abs() + 8)).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_attend_maximum_that_grows_by_less_than_a_rounding(new):
+    """Scores near 2^26.6 (log2 units), where fp32 steps by 8, that grow by one step or two from tile to tile:
+    a weight of 2^8 above the maximum at hand must not overflow. All values are equal, and so is the output."""
+    L, D, page = 64 * 1024, 64, 64
+    n = L // page
+    kp = torch.zeros(n, 1, page, D, dtype=INT8)
+    rung = torch.arange(n) // 2  # a tile of 128 keys is two pages
+    kp[:, 0, :, 0] = 100
+    kp[:, 0, :, 1] = (rung % 100)[:, None].to(INT8)
+    kp[:, 0, :, 2] = (rung // 100 - 2)[:, None].to(INT8)
+    vp = torch.full_like(kp, 77)
+    q = torch.zeros(new, 2, D, dtype=torch.bfloat16)
+    size = 2.0 ** 26.6 / 1.4427 * math.sqrt(D) / 100
+    q[..., 0] = size
+    q[..., 1] = float(q[0, 0, 0]) * 2.0 ** -17
+    q[..., 2] = float(q[0, 0, 0]) * 100 * 2.0 ** -17
+    kp, vp, q = kp.cuda(), vp.cuda(), q.cuda()
+    one = torch.ones(n, 1, device="cuda")
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    for t, max_kv in ((table, L), _wide(table, page)):
+        o, lse, _ = _attend(q, [0, new], [L], t, kp, vp, one, one, max_kv=max_kv)
+        assert bool((o == 77).all()) and torch.isfinite(lse).all()
