@@ -669,10 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       pair_sync();
       top = __vmaxu2(top, row_q[x][half ^ 1][row]);
       const int e = static_cast<int>(imax(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent
-      const int up = imin(254, imax(1, 127 + 14 - (e - 127)));  // 2^(14 - (e - 127)), a normal number
+      const int up = imin(237, 127 + 14 - (e - 127));  // 2^(14 - (e - 127)), at most 2^110 (kv8_decode.cu)
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
       // this row's factor: 2^-e log2(e) / sqrt(D)
-      next_fs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
+      next_fs = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
       auto two = [&](uint32_t u) { return half2_of(bf16_lo(u) * mul, bf16_hi(u) * mul); };
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) {

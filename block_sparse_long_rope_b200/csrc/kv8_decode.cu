@@ -340,10 +340,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = static_cast<int>(imax(top & 0xFFFFu, top >> 16) >> 7);  // biased exponent
-      // 2^(14 - (e - 127)), kept a normal number: subnormal rows stay small
-      const int up = imin(254, imax(1, 127 + 14 - (e - 127)));
+      // 2^(14 - (e - 127)), at most 2^110: that makes any bf16 number fp16 (subnormal ones
+      // are multiples of 2^-133), and its reciprocal times scale_log2 stays normal
+      const int up = imin(237, 127 + 14 - (e - 127));
       const float mul = __uint_as_float(static_cast<uint32_t>(up) << 23);
-      qscale[nt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(imax(1, 254 - up)) << 23);
+      qscale[nt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         qf[nt][i][0] = pack_half2(bf16_lo(w[2 * i]) * mul, bf16_hi(w[2 * i]) * mul);

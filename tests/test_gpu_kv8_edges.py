@@ -196,3 +196,18 @@ def test_attend_maximum_that_grows_by_less_than_a_rounding(new):
     for t, max_kv in ((table, L), _wide(table, page)):
         o, lse, _ = _attend(q, [0, new], [L], t, kp, vp, one, one, max_kv=max_kv)
         assert bool((o == 77).all()) and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("e", [-96, -100, -110, -113, -116, -126, -130])
+def test_attend_tiny_queries_on_large_keys(new, e):
+    """Rows of q down to subnormal numbers, K scales that bring the scores back to ordinary sizes."""
+    lens, page = [700, 90], 32
+    case = list(_attend_case(lens, [new, new], 8, 2, 64, page, E4M3, 103))
+    up = min(119, -e)  # (a scale that star_kv8_append can write: 2^119 for the largest bf16 numbers)
+    case[0] = (case[0].double() * 2.0 ** e).to(torch.bfloat16)
+    case[5] = (case[5].double().clamp(max=2.0 ** -2) * 2.0 ** up).float()
+    want = U.attend_plain(case[0], case[1], lens, *case[2:])
+    for table, max_kv in ((case[2], 700), _wide(case[2], page)):
+        o, lse, _ = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)
+        U.check_attend(o, lse, want)
