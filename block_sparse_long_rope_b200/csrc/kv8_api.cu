@@ -352,16 +352,21 @@ star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_toke
   // what the kernels count in 32 bits: rows of a request, tiles of a call
   if ((long long)max_new * g > (1 << 24))
     return fail(STAR_ERR_INVALID_ARG, "max_new * Hq / Hkv (%lld) must be at most 2^24", (long long)max_new * g);
-  // tiles of a call with row tiles of this many rows
+  // tiles of a call with row tiles of this many rows, were every request as long as
+  // the bounds allow
   auto tiles_with = [&](int rows) {
     return (double)B * Hkv * ((max_new * g + rows - 1) / rows) * ((max_kv - 1) / star::kKv8Tile + 1);
+  };
+  // the most that n_tokens tokens can make of them
+  auto most_tiles = [&](int rows) {
+    return fmin(tiles_with(rows), Hkv * ((double)n_tokens * g / rows + B) * ((max_kv - 1) / star::kKv8Tile + 1));
   };
   const size_t need = attend_layout(star::kv8_rows(max_new, g), D).total;
   const int rows = star::kv8_rows(max_new, g) == star::kKv8ChunkRows && tiles_with(16) <= star::kKv8FewTiles
                        ? 16 : star::kv8_rows(max_new, g);
   const AttendLayout lay = attend_layout(rows, D);
-  const double tiles = tiles_with(rows);
-  if (tiles > 2147483647.0)
+  const double tiles = most_tiles(rows);
+  if (tiles >= 2147483647.0)
     return fail(STAR_ERR_INVALID_ARG, "problem too large: %.0f tiles of %d rows by %d keys", tiles,
                 lay.rows, star::kKv8Tile);
   if ((s = check_workspace(workspace, workspace_bytes, need))) return s;

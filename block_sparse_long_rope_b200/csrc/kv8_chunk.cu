@@ -146,10 +146,10 @@ __device__ __forceinline__ bool tiles_before(const Kv8AttendParams& p, int* pref
     const Request r = request_of(p, b, &bad);
     any_bad |= bad;
     int sum = 0;
-    for (int rt = lane; rt < r.row_tiles; rt += 32) sum += tiles_of(p, r, rt);
+    for (int rt = lane; rt < r.row_tiles; rt += 32) sum = add_tiles(sum, tiles_of(p, r, rt));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) prefix[b + 1] = sum * p.Hkv;
+    for (int d = 16; d > 0; d >>= 1) sum = add_tiles(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+    if (lane == 0) prefix[b + 1] = times_tiles(p.Hkv, sum);
   }
   __syncthreads();
   if (warp == 0) {
@@ -159,10 +159,10 @@ __device__ __forceinline__ bool tiles_before(const Kv8AttendParams& p, int* pref
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int up = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += up;
+        if (lane >= d) v = add_tiles(v, up);
       }
-      if (b0 + lane < p.B) prefix[b0 + lane + 1] = base + v;
-      base += __shfl_sync(0xffffffffu, v, 31);
+      if (b0 + lane < p.B) prefix[b0 + lane + 1] = add_tiles(base, v);
+      base = add_tiles(base, __shfl_sync(0xffffffffu, v, 31));
     }
     if (lane == 0) prefix[0] = 0;
   }
@@ -396,6 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
     __syncthreads();
   }
   const int total = prefix[p.B];
+  if (total == kTooManyTiles) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, kDevBounds);
+    return;
+  }
   const int G = imin(static_cast<int>(gridDim.x), total);  // CTAs with work
   if (static_cast<int>(blockIdx.x) >= G) return;
   const int begin = static_cast<int>(static_cast<long long>(blockIdx.x) * total / G);
@@ -892,7 +896,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   Walk w{};
   int begin = 0, first_tile = 0, rows = 0;
   long long last_tile = 0;
-  if (c0 < G) {
+  if (c0 < G && total != kTooManyTiles) {
     begin = static_cast<int>(static_cast<long long>(c0) * total / G);
     const int end = static_cast<int>(static_cast<long long>(c0 + 1) * total / G);
     w = walk_to(p, prefix, end - 1);

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     for (int b = b0; b < b1; ++b) {
       bool bad;
       const Request r = request_of<kRows>(p, b, &bad);
-      mine += p.Hkv * r.row_tiles * r.tiles;
+      mine = add_tiles(mine, times_tiles(p.Hkv, times_tiles(r.row_tiles, r.tiles)));
       any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(p.status, kDevBounds);
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += up;
+      if (lane >= d) inc = add_tiles(inc, up);
     }
     if (lane == 31) warp_tiles[warp] = inc;
     __syncthreads();
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) at += warp_tiles[w];
-      total += warp_tiles[w];
+      total = add_tiles(total, warp_tiles[w]);
     }
     for (int b = b0; b < b1; ++b) {
       bool bad;
@@ -212,6 +212,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT))
     __syncthreads();
   }
   const int total = prefix[p.B];
+  if (total == kTooManyTiles) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(p.status, kDevBounds);
+    return;
+  }
   const int G = imin(static_cast<int>(gridDim.x), total);  // CTAs with work
   if (static_cast<int>(blockIdx.x) >= G) return;
   const int begin = static_cast<int>(static_cast<long long>(blockIdx.x) * total / G);

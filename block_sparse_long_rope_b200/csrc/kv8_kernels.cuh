@@ -22,6 +22,16 @@ __device__ __forceinline__ unsigned inc_acq_rel(unsigned* p, unsigned limit) {
 // The end of what was launched before on the stream (see launch_after).
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Sums of tiles, which stop at INT32_MAX: the host bounds the tiles of offsets that ascend,
+// but others may count tokens many times over. A call whose sum gets there is left out.
+__device__ __forceinline__ int add_tiles(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7FFFFFFFu));
+}
+__device__ __forceinline__ int times_tiles(int heads, int tiles) {
+  return static_cast<int>(min(static_cast<long long>(heads) * tiles, 0x7FFFFFFFll));
+}
+constexpr int kTooManyTiles = 0x7FFFFFFF;
+
 // Where the attention kernels' reference of V scales goes when vs, the largest scale at
 // hand, is above it or 2^12 below it: to vs, but no further than 2^64 below top, the
 // largest so far. O is held in units of the reference: at most 2^24 for each of 2^31

@@ -211,3 +211,40 @@ def test_attend_tiny_queries_on_large_keys(new, e):
     for table, max_kv in ((case[2], 700), _wide(case[2], page)):
         o, lse, _ = _attend(case[0], case[1], lens, table, *case[3:], max_kv=max_kv)
         U.check_attend(o, lse, want)
+
+
+# ---- many tiles ------------------------------------------------------------------------------------------
+def test_attend_a_prompt_among_many_decoding_requests_under_wide_bounds():
+    """One request may bring 4096 tokens and any may have a million keys: with 512 requests that would be 2^31
+    tiles, but the call's tokens can make only some thousands."""
+    g, B, page = torch.Generator().manual_seed(109), 512, 128
+    lens = torch.randint(1, 400, (B,), generator=g).tolist()
+    new = [1] * B
+    lens[77], new[77] = 700, 600
+    q, cu, table, kp, vp, ks, vs = _attend_case(lens, new, 32, 8, 64, page, E4M3, 109)
+    wide = torch.full((B, (1 << 20) // page), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    o, lse, ws = _attend(q, cu, lens, wide, kp, vp, ks, vs, max_new=4096, max_kv=1 << 20)
+    U.check_attend(o, lse, U.attend_plain(q, cu, lens, table, kp, vp, ks, vs))
+    assert _status(ws) == "STAR_OK"
+
+
+@pytest.mark.parametrize("run,T,Hkv,g", [(1, 1024, 8, 8), (50, 4, 64, 8)])
+def test_attend_offsets_that_count_tokens_many_times(run, T, Hkv, g):
+    """Offsets that start again from 0 after every `run` requests make more tiles than the call's tokens can, here
+    2^31 and more: the call is left out and recorded, by either kernel."""
+    B, D, page, L = 4096, 64, 128, 7996 * 128 if run > 1 else 1 << 20
+    cu = [(i % (run + 1)) * T for i in range(B + 1)]
+    n, rows = max(cu), 16 if T * g <= 32 else 256
+    good = sum(b > a for a, b in zip(cu, cu[1:]))
+    assert good * Hkv * -(-T * g // rows) * ((L - T) // 128) > 1.5 * 2 ** 31
+    kp, ks = U.make_pages(2, Hkv, page, D, INT8, 1)
+    table = torch.full((B, L // page), 2 ** 30, dtype=torch.int32, device="cuda")
+    q = torch.zeros(n, Hkv * g, D, dtype=torch.bfloat16, device="cuda")
+    o, lse, ws = _attend(q, cu, [L] * B, table, kp, kp, ks, ks, max_new=T, max_kv=L, fill=3.0)
+    assert _status(ws) == BOUNDS and bool((o == 3.0).all()) and bool((lse == 3.0).all())
+    # the workspace serves the next call
+    case = _attend_case([300], [T], Hkv * g, Hkv, D, page, INT8, 113)
+    o, lse, _ = _attend(case[0], case[1], [300], *case[2:], ws=ws)
+    assert _status(ws) == "STAR_OK"
+    U.check_attend(o, lse, U.attend_plain(case[0], case[1], [300], *case[2:]))
