@@ -340,8 +340,9 @@ star_status star_kv8_attend(const void* q, const int64_t q_stride[2], int n_toke
     return fail(STAR_ERR_INVALID_ARG, "max_pages (%d) must be >= 1 and max_pages * page_len fit int32", max_pages);
   if (n_tokens < 0) return fail(STAR_ERR_INVALID_ARG, "n_tokens must be >= 0");
   if (max_new < 1) return fail(STAR_ERR_INVALID_ARG, "max_new must be >= 1");
-  if (max_kv < 1 || max_kv > ((long long)max_pages << shift))
-    return fail(STAR_ERR_INVALID_ARG, "max_kv (%d) must lie in [1, max_pages * page_len]", max_kv);
+  // (keys and the ends of their tiles are counted in int32)
+  if (max_kv < 1 || max_kv > ((long long)max_pages << shift) || max_kv > INT32_MAX - 2 * star::kKv8Tile)
+    return fail(STAR_ERR_INVALID_ARG, "max_kv (%d) must lie in [1, max_pages * page_len], at most 2^31 - 257", max_kv);
   if ((s = check_strides(q_stride, 2, "q_stride"))) return s;
   if ((s = check_ptr(cu_new, "cu_new", 4)) || (s = check_ptr(kv_len, "kv_len", 4)) ||
       (s = check_ptr(block_table, "block_table", 4)))

@@ -578,19 +578,19 @@ size_t star_kv8_attend_workspace_bytes(int B, int n_tokens, int Hq, int Hkv, int
  *   o [n_tokens, Hq, D] bf16, lse [Hq, n_tokens] fp32 (NULL to skip)
  * Rows from cu_new[B] on are left as they are, and so is what lies in pages
  * behind kv_len, which may hold anything. o and lse overlap no input. max_new
- * bounds T, and max_kv kv_len (1 .. max_pages * page_len): they choose kernels
- * and grids, lengths beyond them are an error. max_new * Hq / Hkv is at most 2^24,
- * and a call is refused where Hkv * (n_tokens * Hq / Hkv / R + B) * max_kv / 128
- * reaches 2^31, R the rows of a tile (8 up to 8 rows of a KV head and request, 16 up
- * to 32, then 256). Scores are fp32 sums of exact products (the codes enter the
- * tensor cores unrounded, and so does q down to 2^-29 of its row's largest
- * element). Weights, times the ratio of their V scale to a reference, are rounded
- * to fp16 under 2^11: 11 bits of a weight down to 2^-25 of the largest, 2^-36 of
- * the largest below that. The reference is at most
- * 2^12 times the largest scale of 128 keys, or 2^-64 of the request's largest.
- * Sums and statistics are fp32. A NaN code reaches only the rows that see its
- * key. Results do not depend on the order in which blocks run. The workspace may
- * serve calls of any smaller shapes too.
+ * bounds T, and max_kv kv_len (1 .. max_pages * page_len, at most 2^31 - 257):
+ * they choose kernels and grids, lengths beyond them are an error. max_new * Hq
+ * / Hkv is at most 2^24, and a call is refused where Hkv * (n_tokens * Hq / Hkv
+ * / R + B) * max_kv / 128 reaches 2^31, R the rows of a tile (8 up to 8 rows of
+ * a KV head and request, 16 up to 32, then 256). Scores are fp32 sums of exact
+ * products (the codes enter the tensor cores unrounded, and so does q down to
+ * 2^-29 of its row's largest element). Weights, times the ratio of their V scale
+ * to a reference, are rounded to fp16 under 2^11: 11 bits of a weight down to
+ * 2^-25 of the largest, 2^-36 of the largest below that. The reference is at
+ * most 2^12 times the largest scale of 128 keys, or 2^-64 of the request's
+ * largest. Sums and statistics are fp32. A NaN code reaches only the rows that
+ * see its key. Results do not depend on the order in which blocks run. The
+ * workspace may serve calls of any smaller shapes too.
  * A request whose lengths or rows of q do not fit is left out, a page index
  * outside the pages makes its keys invisible; both record
  * STAR_ERR_DEVICE_BOUNDS.
