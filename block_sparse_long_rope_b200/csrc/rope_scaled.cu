@@ -9,7 +9,8 @@
 // element within E of a rounding boundary is recomputed in fp64 and rounded
 // once. m is folded into the fp32 cosine and sine, one more rounding of 2^-25
 // that the bound has room for (2^-25 for cos, 2^-25 for m cos, two of 2^-24 for
-// product and sum stay below 2^-22).
+// product and sum stay below 2^-22). The bound is taken as 2^-23 of 2 |m| (|a| + |b|),
+// which is infinite where a product could leave fp32: such a pair goes to fp64 too.
 //
 // Bound: HBM, 4 bytes an element. A unit is 16 elements of a head row: 8 pairs
 // (of the half layout two 16-byte vectors rot/2 apart, of the interleaved one two
@@ -101,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
       c[2 * j] = v.x, s[2 * j] = v.y, c[2 * j + 1] = v.z, s[2 * j + 1] = v.w;
     }
   }
-  const float bound = 2.3841858e-07f * p.mscale_abs;
+  const float reach = 2.f * p.mscale_abs;
+  constexpr float kErr = 1.1920929e-07f;  // 2^-23
 
   // Units of a row's copied part and its pairs sit in different lanes of a warp
   while (h < h_end) {
@@ -127,10 +129,10 @@ __global__ void __launch_bounds__(kThreads, 4) rope_scaled_kernel(const __grid_c
         for (int j = 0; j < 8; ++j) {
           float a, bb;
           elem(j, a, bb);
-          const float e = bound * (fabsf(a) + fabsf(bb));
+          const float t = reach * (fabsf(a) + fabsf(bb));
           const float y0 = fmaf(a, c[j], -(bb * s[j])), y1 = fmaf(bb, c[j], a * s[j]);
-          out[j] = pack_bf16x2(y0 - e, y1 - e);
-          if (out[j] != pack_bf16x2(y0 + e, y1 + e)) bad |= 1u << j;
+          out[j] = pack_bf16x2(fmaf(t, -kErr, y0), fmaf(t, -kErr, y1));
+          if (out[j] != pack_bf16x2(fmaf(t, kErr, y0), fmaf(t, kErr, y1))) bad |= 1u << j;
         }
         if (bad) {
 #pragma unroll

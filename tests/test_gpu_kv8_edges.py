@@ -248,3 +248,31 @@ def test_attend_offsets_that_count_tokens_many_times(run, T, Hkv, g):
     o, lse, _ = _attend(case[0], case[1], [300], *case[2:], ws=ws)
     assert _status(ws) == "STAR_OK"
     U.check_attend(o, lse, U.attend_plain(case[0], case[1], [300], *case[2:]))
+
+
+# ---- rotary near the largest number ------------------------------------------------------------------
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("m", [1.0, 1.5, 2.0, -3.0, 1e30])
+def test_rope_scaled_large_values(inter, m):
+    """Products that leave fp32 while the rotated value does not: the correctly rounded bf16 all the same."""
+    D, S = 64, 41
+    f = [math.pi / 4, 0.5, 1.0, 0.25, 0.1, 1.5, 2.0, 3.0]
+    x = torch.zeros(1, S, 2, D, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(107)
+    x[...] = (torch.randn(x.shape, generator=g) * 2.0 ** 126).clamp(-3.3e38, 3.3e38).to(torch.bfloat16)
+    x[0, :, 0, :16] = 2.97e38  # a pair of equal numbers, turned by pi / 4 at position 1: 0 and its diagonal
+    y = torch.empty_like(x)
+    pos = torch.arange(S, dtype=torch.int32, device="cuda")
+    star.star_rope_scaled(x, y, f, mscale=m, interleaved=inter, pos=pos)
+    i, j = (slice(0, 16, 2), slice(1, 16, 2)) if inter else (slice(0, 8), slice(8, 16))
+    ang = pos.double()[:, None] * torch.tensor(f, dtype=torch.float64, device="cuda")
+    c, s = (m * t(ang)[None, :, None] for t in (torch.cos, torch.sin))
+    a, b = x[..., i].double(), x[..., j].double()
+    want = x.double().clone()
+    want[..., i], want[..., j] = a * c - b * s, b * c + a * s
+    # from 2^128 - 2^119 on, half a step above the largest bf16 number, a value is rounded to infinity
+    err = 1e-12 * abs(m) * 2.0 ** 128
+    top, a = 2.0 ** 128 - 2.0 ** 119, want.abs()
+    assert bool(torch.isinf(y)[a - err >= top].all()) and not torch.isnan(y).any()
+    fits = a + err < top
+    assert bool(((y.double() - want).abs() <= 2.0 ** -8 * a + err)[fits].all())
