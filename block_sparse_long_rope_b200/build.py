@@ -10,8 +10,13 @@ stale objects (or objects built from other sources) is therefore rebuilt. The
 library's star_version() string ends with that digest, so a process can check
 that the library it loaded was built from the sources in this tree
 (`loaded_matches_sources`).
+
+The torch binding's native half (_native.so) is compiled beside it, at the same
+time. Without torch only the library is built: the C ABI needs no more.
 """
+import concurrent.futures
 import hashlib
+import importlib.util
 import os
 import subprocess
 import sys
@@ -86,15 +91,23 @@ def _read(path):
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        native = pool.submit(build_native, force) if importlib.util.find_spec("torch") else None
+        build_library(force, verbose_ptxas)
+        if native:
+            native.result()
+    return LIB
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     hdrs = _header_paths()
     digest = source_digest()
-    objs = []
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    for src in SOURCES:
+
+    def compile_one(src):
         path = os.path.join(CSRC, src)
         obj = os.path.join(OBJ_DIR, src.replace(".cu", ".o"))
-        objs.append(obj)
         defs = [f"-DSTAR_BUILD_DIGEST=\"{digest}\""] if src == "api.cu" else []
         want = _sha([path] + hdrs, ARCH + FLAGS + defs + [_nvcc_version()])
         stamp = obj + ".sha256"
@@ -103,6 +116,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             subprocess.check_call(cmd)
             with open(stamp, "w") as f:
                 f.write(want)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count()) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     lib_stamp = LIB + ".sha256"
     if force or not os.path.exists(LIB) or _read(lib_stamp) != digest:
         tmp = LIB + f".tmp{os.getpid()}"
@@ -111,7 +128,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         os.replace(tmp, LIB)
         with open(lib_stamp, "w") as f:
             f.write(digest)
-    build_native(force)
     return LIB
 
 
