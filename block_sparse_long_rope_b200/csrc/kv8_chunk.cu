@@ -213,23 +213,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// A bounded wait: as mbar_wait, by the SM's clock (%globaltimer takes long to
-// read, and a wait that is not over at once would read it first).
-constexpr long long kWaitClocks = 4000000000ll;  // 2 s at 2 GHz
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 63u) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitClocks) {
-        atomicOr(status, kDevTimeout);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
+  return mbar_wait_clocks(bar, parity, abort, status, kWaitClocks);
 }
 template <int N>
 __device__ __forceinline__ void regs_up() {

@@ -122,19 +122,22 @@ __global__ void debug_index_kernel(int L, int b, int a, int32_t* blk, int32_t* p
   for (int j = 0; j < 4; ++j) ranges[4 * r + j] = out[j];
 }
 
-// One CTA waits, through the same bounded wait the attention and decode
-// kernels use, on an mbarrier that nothing arrives on: after limit_ns the
-// wait gives up and records the time-out in *status; the kernel returns.
+// Two warps of one CTA wait, through the bounded waits that the attention
+// and decode kernels use (by the global timer, and by the SM's clock for as
+// many cycles as limit_ns has nanoseconds), on an mbarrier that nothing
+// arrives on: each gives up after its limit and records the time-out in
+// *status; the kernel returns.
 __global__ void debug_wait_probe_kernel(int* status, unsigned long long limit_ns) {
   __shared__ uint64_t bar;
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag[2];
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
     fence_barrier_init();
-    abort_flag = 0;
+    abort_flag[0] = abort_flag[1] = 0;
   }
   __syncthreads();
-  if (threadIdx.x == 0) mbar_wait(&bar, 0, &abort_flag, status, limit_ns);
+  if (threadIdx.x == 0) mbar_wait(&bar, 0, &abort_flag[0], status, limit_ns);
+  if (threadIdx.x == 32) mbar_wait_clocks(&bar, 0, &abort_flag[1], status, static_cast<long long>(limit_ns));
   __syncthreads();
 }
 
@@ -292,7 +295,7 @@ cudaError_t launch_chunk_finish(const float* sub_o, const float* sub_lse, int ns
 }
 
 cudaError_t launch_debug_wait_probe(int* status, unsigned long long limit_ns, cudaStream_t stream) {
-  debug_wait_probe_kernel<<<1, 32, 0, stream>>>(status, limit_ns);
+  debug_wait_probe_kernel<<<1, 64, 0, stream>>>(status, limit_ns);
   return cudaGetLastError();
 }
 

@@ -276,3 +276,66 @@ def test_rope_scaled_large_values(inter, m):
     assert bool(torch.isinf(y)[a - err >= top].all()) and not torch.isnan(y).any()
     fits = a + err < top
     assert bool(((y.double() - want).abs() <= 2.0 ** -8 * a + err)[fits].all())
+
+
+# ---- bounded waits ---------------------------------------------------------------------------------------
+def test_both_bounded_waits_give_up():
+    """The wait by the SM's clock that the chunk kernel uses ends as the one by the global timer does: the
+    call lasts as long as the longer of both, 50 ms and 50 million cycles."""
+    ws = star.alloc_workspace(256)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    star.star_debug_wait_probe(ws, seconds=0.05)
+    b.record()
+    assert _status(ws) == "STAR_ERR_DEVICE_TIMEOUT" and _status(ws) == "STAR_OK"
+    assert 49.0 < a.elapsed_time(b) < 1000.0
+
+
+# ---- together with the calls on a bf16 cache ---------------------------------------------------------------
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_a_phase1_context_moved_into_pages(kind):
+    """A context encoded by Phase 1, its bf16 cache (keys rotated) moved into 8-bit pages in one append per
+    sequence, and new tokens that attend over both."""
+    B, L, Hq, Hkv, D, page, T, theta = 2, 700, 8, 2, 128, 32, 5, 5e5
+    g = torch.Generator().manual_seed(127)
+    rand = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    q, k, v = rand(B, L, Hq, D), rand(B, L, Hkv, D), rand(B, L, Hkv, D)
+    o = torch.empty_like(q)
+    kc, vc = (torch.zeros(B, Hkv, L + 44, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws1 = star.alloc_workspace(star.star_phase1_workspace_bytes(B, L, Hq, D))
+    star.star_phase1_encode(q, k, v, o, kc, vc, 256, 128, theta, ws1)
+    n_pages, W = 60, 30
+    kp, vp = (torch.zeros(n_pages, Hkv, page, D, dtype=kind, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(n_pages, Hkv, device="cuda") for _ in range(2))
+    table, length, begin = ints([[-1] * W] * B), ints([0] * B), ints([0])
+    free = torch.randperm(n_pages, generator=g).to(torch.int32).cuda()
+    shadow, sk, sv = [U.Pages(kp), U.Pages(vp)], ks.double().cpu(), vs.double().cpu()
+    ws = star.alloc_workspace(star.star_kv8_attend_workspace_bytes(B, B * T, Hq, Hkv, D, T))
+
+    def plan(new):
+        n = sum(new)
+        t = [ints([0] * (B + 1)), ints([0] * n), ints([0] * n),
+             ints([0] * (star.star_batch_plan_runs(n, B, page) + 1))]
+        star.star_batch_plan(length, ints(new), free, begin, page, table, *t, length, begin, ws)
+        return t
+
+    def append(rows_k, rows_v, slot, runs):
+        star.star_kv8_append(rows_k, rows_v, slot, runs, kp, vp, ks, vs, ws)
+        U.append_plain(rows_k.double().cpu(), runs.cpu().tolist(), slot.cpu().tolist(), shadow[0], sk, page)
+        U.append_plain(rows_v.double().cpu(), runs.cpu().tolist(), slot.cpu().tolist(), shadow[1], sv, page)
+
+    for b in range(B):  # (a sequence's cache is [Hkv, rows, D]: its rows are a strided view)
+        _, _, slot, runs = plan([L if i == b else 0 for i in range(B)])
+        append(kc[b].transpose(0, 1)[:L], vc[b].transpose(0, 1)[:L], slot, runs)
+    cu, pos, slot, runs = plan([T] * B)
+    x = rand(1, B * T, Hq + 2 * Hkv, D)
+    f, m = star.star_rope_frequencies(D, theta)
+    star.star_rope_scaled(x[:, :, :Hq + Hkv], x[:, :, :Hq + Hkv], f, m, pos=pos)
+    append(x[0, :, Hq:Hq + Hkv], x[0, :, Hq + Hkv:], slot, runs)
+    for got, want in ((kp, shadow[0].values), (vp, shadow[1].values), (ks, sk), (vs, sv)):
+        assert torch.equal(got.double().cpu(), want)
+    out = torch.empty(B * T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(Hq, B * T, device="cuda")
+    star.star_kv8_attend(x[0, :, :Hq], cu, length, table, kp, vp, ks, vs, out, ws, T, W * page, lse=lse)
+    assert _status(ws) == "STAR_OK" and length.cpu().tolist() == [L + T] * B
+    U.check_attend(out, lse, U.attend_plain(x[0, :, :Hq], cu.cpu().tolist(), [L + T] * B, table, kp, vp, ks, vs))
