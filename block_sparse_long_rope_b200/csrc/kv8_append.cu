@@ -14,7 +14,9 @@
 // Bound: HBM, 2 bytes read and 1 written an element. A CTA takes one (run,
 // head, K or V): its threads hold the whole piece in registers between the
 // maximum and the rounding, so each element is read once. 16K tokens of 8 heads of
-// 128, K and V (101 MB): 15.6 us, 6.45 TB/s; 16 decode rows 2.6 us.
+// 128, K and V (101 MB): 18.9 us with other inputs each time (int8, whose conversions
+// are four to e4m3's two packed ones: 23.9), 15.8 us for one graph replayed, part of
+// whose inputs stay in the L2; 16 decode rows 2.5 us.
 #include "kv8_codes.cuh"
 #include "kv8_kernels.cuh"
 #include "star_index.cuh"

@@ -7,7 +7,9 @@
 // scores are 2048 cycles of either); what it spends now is the chain of one slot,
 // score products, softmax, weight products, about 5000 cycles a tile for both
 // slots out of step. 256 tokens of 64 heads after 128K keys of 8 heads (1.1
-// TFLOP): 1320 us, 833 TFLOP/s.
+// TFLOP): 1315 us, 837 TFLOP/s (1410 to 1430 where every call has new inputs); in int8
+// 1330, at D 64 1395 (e4m3) and 1368 (int8). <128, e4m3> spills 118 bytes of stores and
+// 184 of loads a thread, int8 40 and 120: the rest is the way out with NaN codes.
 //  * The T * g (token, query head) rows of a (request, KV head) are cut into
 //    tiles of 256 rows, two slots of 128: a K or V tile of 128 keys is read and
 //    converted once for both.

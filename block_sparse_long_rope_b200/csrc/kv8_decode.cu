@@ -4,10 +4,11 @@
 // with query q sees
 //   s = ks_j (q . K) / sqrt(D),  o = sum e^(s - m) vs_j V / sum e^(s - m).
 // Bound: HBM, one byte an element of K and V: 1M tokens of 8 heads of 128 (2.15 GB)
-// take 333 us, 6.45 TB/s, where a loop that only copies takes 309; 16 requests of
-// 1K to 16K tokens (268 MB) 59 us, whose CTAs end between 40 and 59. A short call is
-// latency: 501 tokens of one head 7.1 us, of which one tile alone is 4.9. The design
-// keeps the stream going:
+// take 329 us, 6.5 TB/s, where a loop that only copies takes 309 (348 behind a kernel
+// that leaves the L2 full of its writes, which go out meanwhile; 355 to 380 where every
+// call has new inputs); 16 requests of 1K to 16K tokens (268 MB) 59 us, whose CTAs end
+// between 40 and 59. A short call is latency: 501 tokens of one head 7.0 to 7.5 us, of
+// which one tile alone is 4.9. The design keeps the stream going:
 //  * The T * g (token, query head) rows of a (request, KV head) form one tile of
 //    8 or 16 rows, so each code is read once for all of them; further rows make
 //    further tiles.
@@ -50,8 +51,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
 // 16 rows of D 128 hold 64 accumulators and 32 words of q a thread: within 128
-// registers they spill (16 rows over 100K keys of 8 heads: 88 us instead of 64; at
-// D 64 it fits and takes 42 us instead of 53).
+// registers they spill throughout (16 rows over 100K keys of 8 heads: 88 us instead of
+// 65). At D 64 the spills are few (28 bytes of stores and 52 of loads for e4m3) and two
+// CTAs take 41 us instead of 53; 8 rows of D 128 in e4m3 spill 20 and 36.
 __host__ __device__ constexpr int ctas_per_sm(int D, int NT) { return NT == 1 || D == 64 ? 2 : 1; }
 constexpr float kPShift = 11.f;  // P is held as 2^11 e^(s - m)
 constexpr float kSlack = 4.f;    // growth of the maximum (log2) before it moves

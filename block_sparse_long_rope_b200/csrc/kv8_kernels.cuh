@@ -125,18 +125,19 @@ constexpr int kKv8MaxCtas = 512;  // the workspace holds parts for this many (de
 constexpr int kKv8ChunkRows = 256, kKv8ChunkMaxCtas = 160;
 // Rows of a (request, KV head) tile: 8 or 16 of the decode kernel, or the chunk
 // kernel's. Up to 32 rows two decode tiles read the pages twice and still win: 20
-// rows over 128K keys of 8 heads take 133 us against 176, over 2000 keys 17 against
-// 22. At 40 rows three tiles take 189 us against 179 (16 requests of 16K: 251
-// against 205).
+// rows over 128K keys of 8 heads take 133 us against 168, over 2000 keys 16.5 against
+// 21.4. At 40 rows three tiles take 190 us against 168 (16 ragged requests up to 16K:
+// 254 against 188). None of these is near its bytes, 41 us over 128K keys: 8 rows take
+// 55 us, 16 rows 77.
 inline int kv8_rows(int max_new, int g) {
   const long long rows = (long long)max_new * g;
   return rows <= 8 ? 8 : rows <= 32 ? 16 : kKv8ChunkRows;
 }
 // A call of more rows stays on the decode kernel while it has at most this many
 // tiles of 16 rows by 128 keys, since the chunk kernel needs 15 us before its first
-// product: 240 rows on 3000 keys of D 64 (360 tiles) 15.5 us against 25, 200 rows of
-// 8 heads on 1000 keys (832) 21.7 against 25; 40 rows of 16 requests, 8 heads on 500
-// keys (1536) 37 against 31, 1024 rows of 8 heads on 600 keys (2560) 48 against 34.
+// product: 240 rows on 3000 keys of D 64 (360 tiles) 17 us against 27, 200 rows of 8
+// heads on 1000 keys (832) 22 against 26; 40 rows of 16 requests, 8 heads on 500 keys
+// (1536) 36 against 37, 1024 rows of 8 heads on 600 keys (2560) 48 against 36.
 constexpr int kKv8FewTiles = 1024;
 cudaError_t launch_kv8_decode(const Kv8AttendParams& p, int D, int kv_type, int rows, int sms,
                               cudaStream_t stream);

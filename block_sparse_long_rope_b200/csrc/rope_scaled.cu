@@ -18,8 +18,11 @@
 // walks over heads, its 8 cosines and sines in registers; the CTA builds them
 // once in shared memory, with their fp64 values for the slow path. The rounding
 // test takes both ends of the error interval as packed bf16 pairs and branches
-// once for a unit's 8 pairs. 16K tokens x 40 heads of 128 (336 MB): 61.9 us, 5.4
-// TB/s, two thirds of the issue slots; 16 tokens 3.0 us.
+// once for a unit's 8 pairs. 16K tokens x 40 heads of 128 (336 MB): 62.2 us, 5.4
+// TB/s, two thirds of the issue slots (interleaved 64.8; half of the head 62.2, since
+// copying lanes wait for the pairs of their warp); 16 tokens 3.1 us. A CTA's rows are 8
+// tokens of 4 heads (8 at D 64): with fewer heads than that threads idle, and 16K
+// tokens of 5 heads take 21.8 us, of one 18.4.
 #include <cmath>
 
 #include "kv8_kernels.cuh"
