@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "star_common.cuh"
+
 namespace star {
 
 constexpr int kMaxRequests = 4096;  // requests of one call: their offsets live in shared memory
@@ -21,6 +23,26 @@ __device__ __forceinline__ unsigned inc_acq_rel(unsigned* p, unsigned limit) {
 }
 // The end of what was launched before on the stream (see launch_after).
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A bounded wait as mbar_wait, by the SM's clock: %globaltimer takes long to read, and
+// a wait that is not over at once would read it first.
+constexpr long long kWaitClocks = 4000000000ll;  // 2 s at 2 GHz
+__device__ __forceinline__ bool mbar_wait_clocks(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                                 int* status, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (clock64() - t0 > limit) {
+        atomicOr(status, kDevTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
 
 // Sums of tiles, which stop at INT32_MAX: the host bounds the tiles of offsets that ascend,
 // but others may count tokens many times over. A call whose sum gets there is left out.

@@ -17,6 +17,7 @@
 // HBM-bound and tiny: it reads nsplit * (D + 1) floats per row.
 #include <math.h>
 
+#include "kv8_kernels.cuh"
 #include "star_common.cuh"
 #include "star_kernels.cuh"
 

@@ -82,26 +82,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// The same by the SM's clock: %globaltimer takes long to read, and a wait that is
-// not over at once would read it first.
-constexpr long long kWaitClocks = 4000000000ll;  // 2 s at 2 GHz
-__device__ __forceinline__ bool mbar_wait_clocks(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                                 int* status, long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > limit) {
-        atomicOr(status, kDevTimeout);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------
 // TMA tile loads (no cluster multicast anywhere in this library).
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
