@@ -339,3 +339,44 @@ def test_a_phase1_context_moved_into_pages(kind):
     star.star_kv8_attend(x[0, :, :Hq], cu, length, table, kp, vp, ks, vs, out, ws, T, W * page, lse=lse)
     assert _status(ws) == "STAR_OK" and length.cpu().tolist() == [L + T] * B
     U.check_attend(out, lse, U.attend_plain(x[0, :, :Hq], cu.cpu().tolist(), [L + T] * B, table, kp, vp, ks, vs))
+
+
+# ---- many requests, and two graphs at once ------------------------------------------------------------------
+@pytest.mark.parametrize("long", [1, 16, 77])
+def test_attend_most_requests_of_the_largest_head(long):
+    """4096 requests of D 128, whose offsets take the most shared memory beside either kernel's tiles."""
+    g = torch.Generator().manual_seed(131)
+    lens = torch.randint(0, 60, (4096,), generator=g).tolist()
+    new = [min(1, L) for L in lens]
+    lens[1234], new[1234] = 300, long
+    case = _attend_case(lens, new, 2, 1, 128, 16, E4M3, 131)
+    o, lse, ws = _attend(case[0], case[1], lens, *case[2:])
+    assert _status(ws) == "STAR_OK"
+    U.check_attend(o, lse, U.attend_plain(case[0], case[1], lens, *case[2:]))
+
+
+@pytest.mark.parametrize("new", [1, 16, 70])
+def test_attend_two_graphs_replayed_at_once(new):
+    """Two captured calls with a workspace each, replayed on two streams at the same time."""
+    lens = [9000, 700, 20000]
+    q, cu, *rest = _attend_case(lens, [new] * 3, 8, 2, 128, 64, E4M3, 137)
+    want, want_lse, _ = _attend(q, cu, lens, *rest)
+    cu_t, kv_t = ints(cu), ints(lens)
+    sides = []
+    for _ in range(2):
+        ws = star.alloc_workspace(star.star_kv8_attend_workspace_bytes(3, 3 * new, 8, 2, 128, new))
+        o, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(5):
+                star.star_kv8_attend(q, cu_t, kv_t, *rest, o, ws, new, max(lens), lse=lse)
+        sides.append((torch.cuda.Stream(), graph, o, lse, ws))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for stream, graph, *_ in sides:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, o, lse, ws in sides:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse) and _status(ws) == "STAR_OK"
