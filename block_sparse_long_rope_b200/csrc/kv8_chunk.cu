@@ -218,6 +218,28 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
   return mbar_wait_clocks(bar, parity, abort, status, kWaitClocks);
 }
+// A wait that lasts while the count moves: its limit starts again with every step seen.
+__device__ __forceinline__ bool wait_moving(uint64_t* bar, uint32_t parity, volatile int* abort, volatile int* count,
+                                         int* status) {
+  int seen = *count;
+  long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 63u) == 0) {
+      if (*abort) return false;
+      const int now = *count;
+      if (now != seen) {
+        seen = now;
+        t0 = clock64();
+      }
+      if (clock64() - t0 > kWaitClocks) {
+        atomicOr(status, kDevTimeout);
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -344,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
   __shared__ uint64_t k_full[S], v_full[S], empty[S], sc_full[kRing], nan_full[kRing], lead[kRing];
   __shared__ __align__(16) Scales ring[kRing];
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
+  __shared__ volatile int abort_flag, mma_step;  // mma_step: the second slot's MMA warp moves
   // what a row's two threads exchange
   __shared__ float row_l[2][2][128], row_m[2][2][2][128];
   __shared__ uint32_t row_q[2][2][128];
@@ -378,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
         mbar_init(&lead[s], 1);
       }
       fence_barrier_init();
-      abort_flag = 0;
+      abort_flag = mma_step = 0;
     }
     __syncthreads();
   }
@@ -426,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       uint32_t cnt = 0, segs = 0;  // tiles and segments of this slot so far
       int now = 0;                 // no tile before the first
       for (int n = -1; n < N; ++n) {
+        if (x == 1) mma_step = n;
         // products of a step: PV(n), S(n + 1)
         int next = 0;
         if (n + 1 < N) {
@@ -694,7 +717,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
       // the ring may have passed since its last tile, and a wait by parity takes only
       // one for its own, so a segment begins with the wait for its first scores: they
       // are there after the tile's scales, and no later round is until P answers them.
-      if (active) ok &= warp_wait(&s_full[x], cnt & 1, &abort_flag, p.status);
+      // The skipped tiles may take longer than a wait may, so its limit starts again
+      // whenever the slot's MMA warp has moved.
+      if (active) ok &= __all_sync(0xffffffffu, wait_moving(&s_full[x], cnt & 1, &abort_flag, &mma_step, p.status));
       if (active)  // (a loop of its own: with the test in its condition the kernel takes 2% longer)
 #pragma unroll 1
       for (int i = 0; i < seg; ++i) {

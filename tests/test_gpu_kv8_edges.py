@@ -380,3 +380,26 @@ def test_attend_two_graphs_replayed_at_once(new):
     torch.cuda.synchronize()
     for _, _, o, lse, ws in sides:
         assert torch.equal(o, want) and torch.equal(lse, want_lse) and _status(ws) == "STAR_OK"
+
+
+def test_attend_a_slot_idle_for_longer_than_a_wait():
+    """4096 requests of one token over a long shared prefix leave the second slot idle for over 2 s, the limit of a
+    bounded wait; the last request, of 300 tokens, needs it."""
+    B, Hkv, D, page, L, T = 4096, 8, 64, 128, 655360, 300
+    kp, ks = U.make_pages(7, Hkv, page, D, INT8, 139)
+    vp, vs = U.make_pages(7, Hkv, page, D, INT8, 140)
+    table = (torch.arange(L // page, dtype=torch.int32, device="cuda") % 4)[None].repeat(B, 1)
+    table[-1, :4] = ints([6, 4, 5, 4])
+    lens, new = [L] * (B - 1) + [500], [1] * (B - 1) + [T]
+    cu = list(range(B)) + [B - 1 + T]
+    g = torch.Generator().manual_seed(141)
+    q = torch.randn(B - 1 + T, Hkv, D, generator=g).to(torch.bfloat16).cuda()
+    q[:B - 1] = q[:1]
+    o, lse, ws = _attend(q, cu, lens, table, kp, vp, ks, vs)
+    assert _status(ws) == "STAR_OK"
+    want = U.attend_plain(q[B - 1:], [0, T], [500], table[-1:], kp, vp, ks, vs)
+    U.check_attend(o[B - 1:], lse[:, B - 1:], want)
+    # the other requests are all alike, whichever CTAs share them
+    few = U.attend_plain(q[:1], [0, 1], [L], table[:1], kp, vp, ks, vs)
+    n = B - 1
+    U.check_attend(o[:n], lse[:, :n], [t.expand(n, -1, -1) if t.dim() == 3 else t.expand(-1, n) for t in few])
