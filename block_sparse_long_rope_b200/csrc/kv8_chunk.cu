@@ -767,9 +767,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_chunk_kernel(const __grid_con
           if (up) {
             const bool none = m == -INFINITY;  // nothing seen so far
             m = mt;
-            // P = 2^(s - rf); where m is so large that m - 11 is rounded, rf = m
+            // P = 2^(s - rf) up to 2^15.5; where m is so large that m - 11 is rounded to
+            // less than that allows, rf = m
             float nrf = m - kShift;
-            if (m - nrf > kShift) nrf = m;
+            if (m - nrf > kShift + 0.5f) nrf = m;
             alpha = none ? 1.f : ex2_approx(rf - nrf);
             rf = nrf;
           }

@@ -403,3 +403,42 @@ def test_attend_a_slot_idle_for_longer_than_a_wait():
     few = U.attend_plain(q[:1], [0, 1], [L], table[:1], kp, vp, ks, vs)
     n = B - 1
     U.check_attend(o[:n], lse[:, :n], [t.expand(n, -1, -1) if t.dim() == 3 else t.expand(-1, n) for t in few])
+
+
+# ---- weights far below the largest -----------------------------------------------------------------------
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("kind", [E4M3, INT8])
+def test_attend_small_weights_at_any_maximum(kind, new):
+    """Values only under weights of 2^-20 to 2^-32 of the largest, in rows whose maximum lies between -60 and 60:
+    the weights keep their bits whatever the maximum is (an output in units of 1 would be 2^-36 off)."""
+    L, D, page, Hq = 64, 64, 16, 8
+    n = L // page
+    key = torch.arange(L)
+    k = torch.zeros(L, D)
+    k[:, 0] = 96
+    k[:, 1] = -key.float().div(4, rounding_mode="floor")  # (0 .. -15: codes of either type)
+    v = torch.where((key >= 40)[:, None], torch.randint(-15, 16, (L, D), generator=torch.Generator().manual_seed(149)), 0)
+    pages = lambda x: x.view(n, 1, page, D).to(kind).cuda()  # noqa: E731
+    kp, vp = pages(k), pages(v.float())
+    one = torch.ones(n, 1, device="cuda")
+    rows = new * Hq
+    q = torch.zeros(rows, D)
+    q[:, 0] = torch.linspace(-60, 60, rows) * math.sqrt(D) / 96
+    q[:, 1] = 1.45 * math.sqrt(D)
+    q = q.to(torch.bfloat16).view(new, Hq, D).cuda()
+    table = torch.arange(n, dtype=torch.int32, device="cuda")[None]
+    cu, lens = [0, new], [L + new - 1]  # every row sees the first 64 keys at least
+    if new > 1:  # the new tokens' own keys: far below all others
+        more = -(-(new - 1) // page)
+        k2 = torch.zeros(more * page, D)
+        k2[:, 1] = -120
+        kp = torch.cat([kp, k2.view(more, 1, page, D).to(kind).cuda()])
+        vp = torch.cat([vp, torch.zeros(more, 1, page, D).to(kind).cuda()])
+        one = torch.ones(n + more, 1, device="cuda")
+        table = torch.arange(n + more, dtype=torch.int32, device="cuda")[None]
+    want = U.attend_plain(q, cu, lens, table, kp, vp, one, one)
+    for t, max_kv in ((table, max(lens)), _wide(table, page)):
+        o, lse, _ = _attend(q, cu, lens, t, kp, vp, one, one, max_kv=max_kv)
+        U.check_attend(o, lse, want)
+        # the bound's terms by key are 2^-36 of a code: small beside these outputs
+        assert float((2.0 ** -36 * want[4]).max()) < 0.1 * float(want[0].abs().amax(2).min())
